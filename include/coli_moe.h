@@ -441,6 +441,167 @@ coli_status coli_moe_route_noalloc(const float* router_w, const float* router_bi
                                    float* weights, coli_stream stream);
 
 /*
+ * Operators around the layer, for callers that run experts of their own (in
+ * bf16, with adapters, in training) beside or instead of the int4 ones, and
+ * for blocks whose norms carry gains, gates and scales. None of them needs a
+ * layer or allocates; none synchronises; all can be captured in a CUDA graph.
+ * Common to them:
+ *  - tensors are DEVICE pointers on `device`; a call switches to that device
+ *    and back. `stream` is one of that device's streams.
+ *  - matrices are row-major with `*_stride` elements between rows (>= the
+ *    row's length); fp32 or bf16 (coli_dtype) as their dtype argument says,
+ *    aligned to their element; rows that all start on 16-byte boundaries, with
+ *    hidden % 8 == 0, take the vector path. int32 and fp32 arrays are dense.
+ *  - 0 <= n_tokens <= 2^20, 1 <= top_k <= 32, n_tokens * top_k <= 2^24,
+ *    1 <= n_experts <= 1024, 1 <= hidden <= 65536.
+ *  - an output must not overlap an input or another output unless a call says
+ *    that it may be the same matrix (COLI_EINVAL).
+ *  - arithmetic is fp32, each output rounded once (nearest even) to its type.
+ *    Results are deterministic: no atomics on values, fixed orders of summation.
+ *  - `work` is scratch memory of the caller's, 16-byte aligned, at least as
+ *    large as the operator's workspace function says (a NULL work where that
+ *    is 0), of any contents. It carries nothing from one call to the next, but
+ *    two calls that may overlap on the GPU must not share it.
+ */
+
+/*
+ * Tokens sorted by expert (the router of "Colibri: 2400 lines of pure C ..."
+ * (kechuai.cn), section 一, read as an operator of its own; section 二's
+ * batch-union is the same sort). ids [n_tokens][top_k]: the routing
+ * (coli_moe_route); an id outside [0, n_experts) is an empty slot. Writes
+ *   counts [n_experts], offsets [n_experts + 1]   slots per expert, exclusive scan
+ *   pos [n_tokens][top_k]    row of slot (t, k): offsets[id] + the number of the
+ *                            expert's slots before it in (t, k) order; -1: empty
+ *   slot [n_tokens * top_k]  t * top_k + k of each row; -1 from offsets[n_experts] on
+ *   rows [n_rows][hidden]    rows[pos[t][k]] = x[t], n_rows >= n_tokens * top_k;
+ *                            rows from offsets[n_experts] on are left as they were
+ * One token may hold the same expert twice. x and rows NULL: the plan alone.
+ * dispatch_backward: dx[t] = base[t] + sum over k of drows[pos[t][k]] (base NULL: 0;
+ * positions outside [0, n_rows) add nothing). dx may be base.
+ */
+int64_t coli_moe_dispatch_workspace(int n_tokens, int top_k, int n_experts);
+coli_status coli_moe_dispatch(const int32_t* ids, int n_tokens, int top_k, int n_experts, const void* x,
+                              coli_dtype x_dtype, int64_t x_stride, int hidden, int32_t* counts, int32_t* offsets,
+                              int32_t* pos, int32_t* slot, void* rows, coli_dtype rows_dtype, int64_t rows_stride,
+                              int64_t n_rows, void* work, int64_t work_bytes, int device, coli_stream stream);
+coli_status coli_moe_dispatch_backward(const int32_t* pos, int n_tokens, int top_k, const void* drows,
+                                       coli_dtype rows_dtype, int64_t rows_stride, int64_t n_rows, int hidden,
+                                       const void* base, int64_t base_stride, void* dx, coli_dtype dx_dtype,
+                                       int64_t dx_stride, int device, coli_stream stream);
+
+/*
+ * Expert rows back into their tokens, with the routing weights:
+ *   y[t] = base[t] + sum over k = 0.. of weights[t][k] * rows[pos[t][k]]
+ * in that order (base, of y's type: the shared experts' or the residual's
+ * part; NULL: 0). pos as coli_moe_dispatch wrote it; a position outside
+ * [0, n_rows) adds nothing, whatever its weight. y may be base.
+ * combine_backward, from dy (d loss / d y):
+ *   drows[pos[t][k]] = weights[t][k] * dy[t]
+ *   dweights[t][k]   = dot(dy[t], rows[pos[t][k]]), 0 for an empty slot
+ * (drows or dweights may be NULL; drows has rows' type; rows that no position
+ * names are left as they were; the gradient of base is dy). rows may be NULL
+ * when dweights is NULL. drows may be rows.
+ */
+coli_status coli_moe_combine(const int32_t* pos, const float* weights, int n_tokens, int top_k, const void* rows,
+                             coli_dtype rows_dtype, int64_t rows_stride, int64_t n_rows, int hidden, const void* base,
+                             int64_t base_stride, void* y, coli_dtype y_dtype, int64_t y_stride, int device,
+                             coli_stream stream);
+coli_status coli_moe_combine_backward(const int32_t* pos, const float* weights, int n_tokens, int top_k,
+                                      const void* dy, coli_dtype dy_dtype, int64_t dy_stride, int hidden,
+                                      const void* rows, coli_dtype rows_dtype, int64_t rows_stride, int64_t n_rows,
+                                      void* drows, int64_t drows_stride, float* dweights, int device,
+                                      coli_stream stream);
+
+/*
+ * Gradient of the router (coli_moe_route) from d loss / d weights:
+ *   dlogits[t][k] = w (dw[t][k] - sum_j w[t][j] dw[t][j]),  w = weights[t][k]
+ *   dx[t]         = sum over k of dlogits[t][k] * router_w[ids[t][k]]
+ *   drouter_w[e]  = sum over the slots of e of dlogits * x[t]
+ *   dbias[e]      = sum over the slots of e of dlogits
+ * A slot with an id outside [0, n_experts) or with weight 0 (one that expert
+ * top-p dropped) counts as absent: its dweights is not used, its dlogits is 0.
+ * The selection itself has no gradient. Pass the whole routing, on an
+ * expert-parallel rank too (dweights summed over the ranks first).
+ * ids, weights: as routed; offsets, slot: coli_moe_dispatch's plan of those ids
+ * (not needed when drouter_w and dbias are NULL). dlogits is always written;
+ * dx, drouter_w and dbias may each be NULL. x (used for drouter_w) and dx have
+ * `dtype`. Every element of the outputs is written.
+ */
+int64_t coli_moe_route_backward_workspace(int n_tokens, int top_k, int n_experts, int hidden);
+coli_status coli_moe_route_backward(const float* router_w, int n_experts, int hidden, int top_k, const void* x,
+                                    coli_dtype dtype, int64_t x_stride, int n_tokens, const int32_t* ids,
+                                    const float* weights, const float* dweights, const int32_t* offsets,
+                                    const int32_t* slot, float* dlogits, void* dx, int64_t dx_stride,
+                                    float* drouter_w, float* dbias, void* work, int64_t work_bytes, int device,
+                                    coli_stream stream);
+
+/*
+ * Norms around a block. A block with its norms computes
+ *   x <- x_scale * x + y_scale * token_gate[t] * gate * post(y),  y = Block(norm(x) * pre_gain)
+ * where norm(v) = v / sqrt(mean(v^2) + eps) over the row (RMSNorm) and
+ * post(y) = norm(y) * post_gain when post_norm is 1, else y. Gains and gate
+ * are fp32 [hidden] DEVICE arrays, NULL: 1.
+ */
+typedef struct {
+    const float* pre_gain;
+    const float* post_gain;  /* NULL unless post_norm */
+    const float* gate;
+    float x_scale;           /* residual scale */
+    float y_scale;           /* branch scale   */
+    float eps;               /* >= 0, of both norms */
+    int32_t post_norm;       /* 0 or 1 */
+} coli_block_params;
+
+/*
+ * The norms between two blocks in one pass: the end of block `prev` and the
+ * start of block `next`:
+ *   x_out[t] = prev.x_scale * x[t] + prev.y_scale * token_gate[t] * prev.gate * post(y[t])
+ *   n[t]     = norm(x_out[t]) * next.pre_gain   (of x_out as stored, eps of next)
+ * x, x_out: x_dtype; y: y_dtype; n: n_dtype. token_gate [n_tokens] fp32 or
+ * NULL: 1. prev NULL (before the first block): n = norm(x) * next.pre_gain; y,
+ * x_out and token_gate must be NULL. next NULL (after the last block): n must
+ * be NULL. x_out may be x, n may be y (same pointer, type and stride).
+ * A mean of squares outside fp32's range is summed again in fp64.
+ */
+coli_status coli_block_norm(const coli_block_params* prev, const coli_block_params* next, const void* x,
+                            coli_dtype x_dtype, int64_t x_stride, const void* y, coli_dtype y_dtype, int64_t y_stride,
+                            const float* token_gate, void* x_out, int64_t x_out_stride, void* n, coli_dtype n_dtype,
+                            int64_t n_stride, int n_tokens, int hidden, int device, coli_stream stream);
+
+/*
+ * Its gradient, from dx_out (d loss / d x_out by the paths other than n; NULL:
+ * 0) and dn (d loss / d n). x_out is the forward's (with prev NULL: x) and y
+ * its input; x is not needed. With s = x_out, ds the whole gradient on it:
+ *   ds   = dx_out + d norm(s)^T (next.pre_gain * dn)
+ *   dx   = prev.x_scale * ds  (prev NULL: ds)
+ *   dy   = d post(y)^T (prev.y_scale * token_gate * prev.gate * ds)
+ * and, summed over the tokens, dpre_gain, dpost_gain, dgate [hidden], and
+ * dtoken_gate [n_tokens] (each fp32, or NULL; dpost_gain needs post_norm).
+ * x_out, dx_out, dx: x_dtype; y, dy: y_dtype; dn: n_dtype. dx and dy may be
+ * NULL. dx may be dx_out or x_out, dy may be y or (same type) dn.
+ * work: needed when dpre_gain, dpost_gain or dgate is given.
+ */
+int64_t coli_block_norm_workspace(int n_tokens, int hidden);
+coli_status coli_block_norm_backward(const coli_block_params* prev, const coli_block_params* next, const void* x_out,
+                                     coli_dtype x_dtype, int64_t x_out_stride, const void* y, coli_dtype y_dtype,
+                                     int64_t y_stride, const float* token_gate, const void* dx_out,
+                                     int64_t dx_out_stride, const void* dn, coli_dtype n_dtype, int64_t dn_stride,
+                                     void* dx, int64_t dx_stride, void* dy, int64_t dy_stride, float* dpre_gain,
+                                     float* dpost_gain, float* dgate, float* dtoken_gate, void* work,
+                                     int64_t work_bytes, int n_tokens, int hidden, int device, coli_stream stream);
+
+/*
+ * Residual stack whose blocks carry norms, gates and scales, over fp32
+ * activations, in place: for l = 0..n_layers-1
+ *   x <- x_scale_l * x + y_scale_l * gate_l * post_l(MoE_l(norm(x) * pre_gain_l))
+ * blocks: host array of n_layers parameters. y_work [n_tokens][H] fp32 DEVICE
+ * scratch, not overlapping x. Otherwise as coli_moe_stack_forward; the end of
+ * a block and the start of the next are one pass (coli_block_norm).
+ */
+coli_status coli_moe_block_stack_forward(coli_moe_layer* const* layers, const coli_block_params* blocks, int n_layers,
+                                         float* x, float* y_work, int n_tokens, coli_stream stream);
+
+/*
  * Testing aid for the bounded waits of the kernels that wait on barriers or
  * flags (the integer-MMA persistent kernel, the certified router's GEMM and the
  * tensor-core grouped GEMMs): every wait of their launches on this layer gives

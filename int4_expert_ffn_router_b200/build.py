@@ -21,7 +21,7 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     flags = list(extra or [])
     if os.environ.get("COLI_TC_TRACE") == "1":
         flags.append("-DCOLI_TC_TRACE=1")
-    cmd = ["nvcc", *NVCC_FLAGS, *flags, "-o", SO, *srcs]
+    cmd = ["nvcc", "-t", "0", *NVCC_FLAGS, *flags, "-o", SO, *srcs]
     if verbose:
         print(" ".join(cmd))
     subprocess.check_call(cmd)

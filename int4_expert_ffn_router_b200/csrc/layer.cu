@@ -9,6 +9,7 @@
 #include <string>
 #include <vector>
 
+#include "block.cuh"
 #include "common.cuh"
 #include "expert_cache.h"
 #include "kernels.cuh"
@@ -74,20 +75,6 @@ cudaError_t dev_alloc(T** p, size_t bytes) {
     *p = static_cast<T*>(v);
     return e;
 }
-
-// Switches to `dev` for the lifetime of the guard.
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = true;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-        if (prev != dev) ok = cudaSetDevice(dev) == cudaSuccess;
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
 
 bool is_device_ptr(const void* p) {
     cudaPointerAttributes a;
@@ -898,6 +885,40 @@ COLI_API coli_status coli_moe_stack_forward(coli_moe_layer* const* layers, int n
         L->launches += 1;
         coli_status st = L->cached ? cached_forward(L, L->xn, x, COLI_F32, T, x, s, l + 1 < n_layers ? layers[l + 1] : nullptr)
                                    : forward_impl(L, L->xn, x, COLI_F32, T, x, s);
+        if (st != COLI_OK) return st;
+    }
+    return COLI_OK;
+}
+
+COLI_API coli_status coli_moe_block_stack_forward(coli_moe_layer* const* layers, const coli_block_params* blocks,
+                                                  int n_layers, float* x, float* y_work, int T, coli_stream stream) {
+    if (!layers || !blocks || n_layers < 0) return fail(COLI_EINVAL, "bad layer or block list");
+    if (n_layers == 0 || T == 0) return COLI_OK;
+    if (!x || !y_work) return fail(COLI_EINVAL, "x or y_work is NULL");
+    if (((uintptr_t)y_work) & 15u) return fail(COLI_EINVAL, "y_work must be 16-byte aligned");
+    const coli_moe_layer* L0 = layers[0];
+    for (int l = 0; l < n_layers; ++l) {
+        coli_status st = check_call(layers[l], x, COLI_F32, T);
+        if (st != COLI_OK) return st;
+        if (layers[l]->d.H != L0->d.H || layers[l]->device != L0->device)
+            return fail(COLI_EINVAL, "layers must share hidden size and device");
+        if (const char* m = check_block_params(blocks + l)) return fail(COLI_EINVAL, m);
+    }
+    const int H = L0->d.H;
+    const Mat mx{x, COLI_F32, T, H, H}, my{y_work, COLI_F32, T, H, H};
+    if (overlap(mx, my)) return fail(COLI_EINVAL, "x and y_work overlap");
+    DeviceGuard guard(L0->device);
+    cudaStream_t s = (cudaStream_t)stream;
+    for (int l = 0; l <= n_layers; ++l) {  // the end of block l - 1 and the start of block l in one pass
+        coli_moe_layer* L = l < n_layers ? layers[l] : nullptr;
+        const Mat n{L ? L->xn : nullptr, COLI_F32, T, H, H};
+        coli_status st = block_norm_launch(l > 0 ? blocks + l - 1 : nullptr, L ? blocks + l : nullptr, &mx, &my, &mx, &n,
+                                           nullptr, T, H, s);
+        if (st != COLI_OK) return st;
+        (L ? L : layers[l - 1])->launches += 1;
+        if (!L) break;
+        st = L->cached ? cached_forward(L, L->xn, y_work, COLI_F32, T, nullptr, s, l + 1 < n_layers ? layers[l + 1] : nullptr)
+                       : forward_impl(L, L->xn, y_work, COLI_F32, T, nullptr, s);
         if (st != COLI_OK) return st;
     }
     return COLI_OK;
