@@ -96,23 +96,13 @@ def _load() -> ctypes.CDLL:
     L.coli_moe_layer_create_ep.argtypes = [pcfg, vp, vp, vp, vp, vp, vp, i32, i32, i32, ctypes.POINTER(vp)]
     L.coli_moe_ep_range.argtypes = [i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]
     L.coli_moe_router_fallbacks.argtypes = [vp, ctypes.POINTER(i32), ctypes.POINTER(i32)]
-    i64, pblk = ctypes.c_int64, ctypes.c_void_p
+    i64 = ctypes.c_int64  # the other operators around the layer are called through csrc/binding.cpp
     L.coli_moe_dispatch_workspace.argtypes = [i32, i32, i32]
     L.coli_moe_dispatch_workspace.restype = i64
-    L.coli_moe_dispatch.argtypes = [vp, i32, i32, i32, vp, i32, i64, i32, vp, vp, vp, vp, vp, i32, i64, i64, vp, i64,
-                                    i32, vp]
-    L.coli_moe_dispatch_backward.argtypes = [vp, i32, i32, vp, i32, i64, i64, i32, vp, i64, vp, i32, i64, i32, vp]
-    L.coli_moe_combine.argtypes = [vp, vp, i32, i32, vp, i32, i64, i64, i32, vp, i64, vp, i32, i64, i32, vp]
-    L.coli_moe_combine_backward.argtypes = [vp, vp, i32, i32, vp, i32, i64, i32, vp, i32, i64, i64, vp, i64, vp, i32, vp]
     L.coli_moe_route_backward_workspace.argtypes = [i32, i32, i32, i32]
     L.coli_moe_route_backward_workspace.restype = i64
-    L.coli_moe_route_backward.argtypes = [vp, i32, i32, i32, vp, i32, i64, i32, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp,
-                                          vp, i64, i32, vp]
-    L.coli_block_norm.argtypes = [pblk, pblk, vp, i32, i64, vp, i32, i64, vp, vp, i64, vp, i32, i64, i32, i32, i32, vp]
     L.coli_block_norm_workspace.argtypes = [i32, i32]
     L.coli_block_norm_workspace.restype = i64
-    L.coli_block_norm_backward.argtypes = [pblk, pblk, vp, i32, i64, vp, i32, i64, vp, vp, i64, vp, i32, i64, vp, i64,
-                                           vp, i64, vp, vp, vp, vp, vp, i64, i32, i32, i32, vp]
     L.coli_moe_block_stack_forward.argtypes = [vp, vp, i32, vp, vp, i32, vp]
     L.coli_status_string.argtypes = [i32]
     L.coli_status_string.restype = ctypes.c_char_p
@@ -142,11 +132,11 @@ def _ptr(a) -> int | None:
     return int(a)
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, device=None) -> int | None:
     if stream is None:
         try:
             import torch
-            return torch.cuda.current_stream().cuda_stream
+            return torch.cuda.current_stream(device).cuda_stream
         except Exception:
             return None
     return getattr(stream, "cuda_stream", stream)
@@ -379,82 +369,35 @@ def stack_forward(layers, x, n_tokens: int | None = None, eps: float = 1e-6, str
 # caller's; without `stream` the call goes to the current stream of the
 # tensors' device.
 # ---------------------------------------------------------------------------
-_MAT_DTYPES: dict = {}   # torch dtype -> COLI_* of a matrix (filled on first use)
-_TORCH = None
+_OPS = None
 
 
-def _torch():
-    global _TORCH
-    if _TORCH is None:
-        import torch
-        _MAT_DTYPES.update({torch.float32: F32, torch.bfloat16: BF16})
-        _TORCH = torch
-    return _TORCH
+def _ops():
+    """The module that calls the library with torch tensors (built beside it)."""
+    global _OPS
+    if _OPS is None:
+        import torch  # noqa: F401  (the module links to torch's libraries)
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise ImportError(f"{HERE}/_binding.so is missing or does not load ({e}): build it with "
+                              "__graft_entry__.build()") from e
+        _OPS = _binding
+    return _OPS
 
 
-def _mat(t, name, rows, cols, dev):
-    """(address, dtype code, row stride) of a matrix argument [rows][cols] (None: an absent one);
-    rows None: at least one may differ, the caller checks."""
-    if t is None:
-        return None, F32, cols
-    d = _MAT_DTYPES.get(t.dtype)
-    if d is None:
-        raise TypeError(f"{name} must be float32 or bfloat16, not {t.dtype}")
-    shape = t.shape
-    if len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows):
-        raise ValueError(f"{name} must have shape [{'*' if rows is None else rows}, {cols}], not {list(shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is not on cuda:{dev}")
-    s0, s1 = t.stride()
-    if s1 != 1 and cols > 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    if shape[0] <= 1 and s0 < cols:
-        s0 = cols
-    return t.data_ptr() or None, d, s0
-
-
-def _arr(t, name, shape, dtype, dev):
-    """Address of a dense array argument (None: an absent one)."""
+def _fp32(t, name, shape, dev) -> int | None:
+    """Address of a dense fp32 array argument (None: an absent one)."""
+    import torch
     if t is None:
         return None
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is not on cuda:{dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+        raise TypeError(f"{name} must be a float32 torch tensor")
+    if t.get_device() < 0 or (dev is not None and t.get_device() != dev):
+        raise ValueError(f"{name} must be a CUDA tensor" + ("" if dev is None else f" on cuda:{dev}"))
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of shape {list(shape)}, not {list(t.shape)}")
     return t.data_ptr() or None
-
-
-def _work(t, dev):
-    if t is None:
-        return None, 0
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"work must be a contiguous tensor on cuda:{dev}")
-    return t.data_ptr() or None, t.numel() * t.element_size()
-
-
-def _device_of(t, name) -> int:
-    if t is None or not hasattr(t, "get_device"):
-        raise TypeError(f"{name} must be a torch tensor")
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return dev
-
-
-def _stream_on(stream, dev):
-    if stream is None:
-        return _torch().cuda.current_stream(dev).cuda_stream
-    return getattr(stream, "cuda_stream", stream)
-
-
-def _slots(t, name):
-    if len(t.shape) != 2:
-        raise ValueError(f"{name} must have shape [tokens, top_k], not {list(t.shape)}")
-    return t.shape
 
 
 def dispatch_workspace(n_tokens: int, top_k: int, n_experts: int) -> int:
@@ -468,75 +411,30 @@ def dispatch_workspace(n_tokens: int, top_k: int, n_experts: int) -> int:
 def dispatch(ids, x, n_experts: int, counts, offsets, pos, slot, rows, work=None, stream=None) -> None:
     """Sort tokens by expert: the plan of the routing ``ids`` [T][K] (counts,
     offsets, pos, slot) and rows[pos[t][k]] = x[t]. x and rows None: the plan alone."""
-    i32 = _torch().int32
-    dev = _device_of(ids, "ids")
-    T, K = _slots(ids, "ids")
-    H = x.shape[-1] if x is not None else 1
-    px, dx, sx = _mat(x, "x", T, H, dev)
-    pr, dr, sr = _mat(rows, "rows", None, H, dev)
-    pw, nw = _work(work, dev)
-    _check(lib.coli_moe_dispatch(
-        _arr(ids, "ids", (T, K), i32, dev), T, K, n_experts, px, dx, sx, H, _arr(counts, "counts", (n_experts,), i32, dev),
-        _arr(offsets, "offsets", (n_experts + 1,), i32, dev), _arr(pos, "pos", (T, K), i32, dev),
-        _arr(slot, "slot", (T * K,), i32, dev), pr, dr, sr, 0 if rows is None else rows.shape[0], pw, nw, dev,
-        _stream_on(stream, dev)), "coli_moe_dispatch")
+    st = (_OPS or _ops()).dispatch(ids, x, n_experts, counts, offsets, pos, slot, rows, work, stream)
+    if st:
+        _check(st, "coli_moe_dispatch")
 
 
 def dispatch_backward(pos, drows, dx, base=None, stream=None) -> None:
     """dx[t] = base[t] + sum_k drows[pos[t][k]]."""
-    i32 = _torch().int32
-    dev = _device_of(pos, "pos")
-    T, K = _slots(pos, "pos")
-    H = dx.shape[-1]
-    pr, dr, sr = _mat(drows, "drows", None, H, dev)
-    px, dd, sx = _mat(dx, "dx", T, H, dev)
-    pb, sb = _base(base, dx, "dx", T, H, dev)
-    _check(lib.coli_moe_dispatch_backward(_arr(pos, "pos", (T, K), i32, dev), T, K, pr, dr, sr, drows.shape[0], H, pb,
-                                          sb, px, dd, sx, dev, _stream_on(stream, dev)), "coli_moe_dispatch_backward")
-
-
-def _base(base, out, name, T, H, dev):
-    if base is None:
-        return None, H
-    if base.dtype != out.dtype:
-        raise TypeError(f"base must have {name}'s dtype")
-    p, _, s = _mat(base, "base", T, H, dev)
-    return p, s
+    st = (_OPS or _ops()).dispatch_backward(pos, drows, dx, base, stream)
+    if st:
+        _check(st, "coli_moe_dispatch_backward")
 
 
 def combine(pos, weights, rows, y, base=None, stream=None) -> None:
     """y[t] = base[t] + sum_k weights[t][k] rows[pos[t][k]]."""
-    t = _torch()
-    dev = _device_of(pos, "pos")
-    T, K = _slots(pos, "pos")
-    H = y.shape[-1]
-    pr, dr, sr = _mat(rows, "rows", None, H, dev)
-    py, dy, sy = _mat(y, "y", T, H, dev)
-    pb, sb = _base(base, y, "y", T, H, dev)
-    _check(lib.coli_moe_combine(_arr(pos, "pos", (T, K), t.int32, dev), _arr(weights, "weights", (T, K), t.float32, dev),
-                                T, K, pr, dr, sr, rows.shape[0], H, pb, sb, py, dy, sy, dev, _stream_on(stream, dev)),
-           "coli_moe_combine")
+    st = (_OPS or _ops()).combine(pos, weights, rows, y, base, stream)
+    if st:
+        _check(st, "coli_moe_combine")
 
 
 def combine_backward(pos, weights, dy, rows, drows=None, dweights=None, stream=None) -> None:
     """drows[pos[t][k]] = weights[t][k] dy[t]; dweights[t][k] = dot(dy[t], rows[pos[t][k]])."""
-    t = _torch()
-    dev = _device_of(pos, "pos")
-    T, K = _slots(pos, "pos")
-    H = dy.shape[-1]
-    pg, dg, sg = _mat(dy, "dy", T, H, dev)
-    pr, dr, sr = _mat(rows, "rows", None, H, dev)
-    like = rows if rows is not None else drows
-    n_rows = 0 if like is None else like.shape[0]
-    pd, dd, sd = _mat(drows, "drows", n_rows, H, dev)
-    if rows is not None and drows is not None and dd != dr:
-        raise TypeError("drows must have rows' dtype")
-    if rows is None and dweights is not None:
-        raise ValueError("dweights needs rows")
-    _check(lib.coli_moe_combine_backward(
-        _arr(pos, "pos", (T, K), t.int32, dev), _arr(weights, "weights", (T, K), t.float32, dev), T, K, pg, dg, sg, H, pr,
-        dr if rows is not None else dd, sr, n_rows, pd, sd, _arr(dweights, "dweights", (T, K), t.float32, dev), dev,
-        _stream_on(stream, dev)), "coli_moe_combine_backward")
+    st = (_OPS or _ops()).combine_backward(pos, weights, dy, rows, drows, dweights, stream)
+    if st:
+        _check(st, "coli_moe_combine_backward")
 
 
 def route_backward_workspace(n_tokens: int, top_k: int, n_experts: int, hidden: int) -> int:
@@ -550,24 +448,10 @@ def route_backward_workspace(n_tokens: int, top_k: int, n_experts: int, hidden: 
 def route_backward(router_w, x, ids, weights, dweights, offsets, slot, dlogits, dx=None, drouter_w=None, dbias=None,
                    work=None, stream=None) -> None:
     """Gradient of the router from d loss / d weights; offsets and slot: dispatch's plan of ``ids``."""
-    t = _torch()
-    dev = _device_of(ids, "ids")
-    T, K = _slots(ids, "ids")
-    E, H = router_w.shape
-    f32, i32 = t.float32, t.int32
-    px, dt, sx = _mat(x, "x", T, H, dev)
-    pd, dd, sd = _mat(dx, "dx", T, H, dev)
-    if dx is not None:
-        if x is not None and dd != dt:
-            raise TypeError("dx must have x's dtype")
-        dt = dd
-    pw, nw = _work(work, dev)
-    _check(lib.coli_moe_route_backward(
-        _arr(router_w, "router_w", (E, H), f32, dev), E, H, K, px, dt, sx, T, _arr(ids, "ids", (T, K), i32, dev),
-        _arr(weights, "weights", (T, K), f32, dev), _arr(dweights, "dweights", (T, K), f32, dev),
-        _arr(offsets, "offsets", (E + 1,), i32, dev), _arr(slot, "slot", (T * K,), i32, dev),
-        _arr(dlogits, "dlogits", (T, K), f32, dev), pd, sd, _arr(drouter_w, "drouter_w", (E, H), f32, dev),
-        _arr(dbias, "dbias", (E,), f32, dev), pw, nw, dev, _stream_on(stream, dev)), "coli_moe_route_backward")
+    st = (_OPS or _ops()).route_backward(router_w, x, ids, weights, dweights, offsets, slot, dlogits, dx, drouter_w,
+                                         dbias, work, stream)
+    if st:
+        _check(st, "coli_moe_route_backward")
 
 
 class Block(ctypes.Structure):
@@ -583,38 +467,19 @@ class Block(ctypes.Structure):
         dev = size = None
         ptrs = []
         for t, name in zip(kept, ("pre_gain", "post_gain", "gate")):
-            if t is None:
-                ptrs.append(None)
-                continue
-            if dev is None:
-                dev, size = _device_of(t, name), t.numel()
-            ptrs.append(_arr(t, name, (size,), _torch().float32, dev))
+            ptrs.append(_fp32(t, name, (t.numel() if size is None and hasattr(t, "numel") else size,), dev))
+            if t is not None and dev is None:
+                dev, size = t.get_device(), t.numel()
         super().__init__(*ptrs, x_scale, y_scale, eps, 1 if post_norm else 0)
         self.tensors, self.device, self.hidden, self.address = kept, dev, size, ctypes.addressof(self)
-
-
-def _blocks(prev, next, H, dev):
-    for b in (prev, next):
-        if b is not None and b.device is not None and (b.device != dev or b.hidden != H):
-            raise ValueError(f"the block's gains are not [{H}] on cuda:{dev}")
-    return None if prev is None else prev.address, None if next is None else next.address
 
 
 def block_norm(prev, next, x, y=None, x_out=None, n=None, token_gate=None, stream=None) -> None:
     """The end of block ``prev`` and the start of block ``next`` (either may be None) in one pass:
     x_out = x_scale x + y_scale token_gate gate post(y); n = norm(x_out) pre_gain."""
-    dev = _device_of(x, "x")
-    T, H = x.shape
-    pp, pn = _blocks(prev, next, H, dev)
-    px, dt, sx = _mat(x, "x", T, H, dev)
-    py, dy, sy = _mat(y, "y", T, H, dev)
-    po, do, so = _mat(x_out, "x_out", T, H, dev)
-    if x_out is not None and do != dt:
-        raise TypeError("x_out must have x's dtype")
-    pm, dm, sm = _mat(n, "n", T, H, dev)
-    tg = None if token_gate is None else _arr(token_gate, "token_gate", (T,), _torch().float32, dev)
-    _check(lib.coli_block_norm(pp, pn, px, dt, sx, py, dy, sy, tg, po, so, pm, dm, sm, T, H, dev,
-                               _stream_on(stream, dev)), "coli_block_norm")
+    st = (_OPS or _ops()).block_norm(prev, next, x, y, x_out, n, token_gate, stream)
+    if st:
+        _check(st, "coli_block_norm")
 
 
 def block_norm_workspace(n_tokens: int, hidden: int) -> int:
@@ -628,26 +493,10 @@ def block_norm_workspace(n_tokens: int, hidden: int) -> int:
 def block_norm_backward(prev, next, x_out, y=None, dx_out=None, dn=None, dx=None, dy=None, dpre_gain=None,
                         dpost_gain=None, dgate=None, token_gate=None, dtoken_gate=None, work=None, stream=None) -> None:
     """Gradient of block_norm from dx_out and dn; x_out and y are the forward's (prev None: x_out is its x)."""
-    f32 = _torch().float32
-    dev = _device_of(x_out, "x_out")
-    T, H = x_out.shape
-    pp, pn = _blocks(prev, next, H, dev)
-    ps, ds, ss = _mat(x_out, "x_out", T, H, dev)
-    py, dt, sy = _mat(y, "y", T, H, dev)
-    po, do, so = _mat(dx_out, "dx_out", T, H, dev)
-    pm, dm, sm = _mat(dn, "dn", T, H, dev)
-    px, dd, sx = _mat(dx, "dx", T, H, dev)
-    pe, de, se = _mat(dy, "dy", T, H, dev)
-    if (dx_out is not None and do != ds) or (dx is not None and dd != ds):
-        raise TypeError("dx_out and dx must have x_out's dtype")
-    if dy is not None and y is not None and de != dt:
-        raise TypeError("dy must have y's dtype")
-    pw, nw = _work(work, dev)
-    _check(lib.coli_block_norm_backward(
-        pp, pn, ps, ds, ss, py, dt, sy, _arr(token_gate, "token_gate", (T,), f32, dev), po, so, pm, dm, sm, px, sx, pe, se,
-        _arr(dpre_gain, "dpre_gain", (H,), f32, dev), _arr(dpost_gain, "dpost_gain", (H,), f32, dev),
-        _arr(dgate, "dgate", (H,), f32, dev), _arr(dtoken_gate, "dtoken_gate", (T,), f32, dev), pw, nw, T, H, dev,
-        _stream_on(stream, dev)), "coli_block_norm_backward")
+    st = (_OPS or _ops()).block_norm_backward(prev, next, x_out, y, dx_out, dn, dx, dy, dpre_gain, dpost_gain, dgate,
+                                              token_gate, dtoken_gate, work, stream)
+    if st:
+        _check(st, "coli_block_norm_backward")
 
 
 def block_stack_forward(layers, blocks, x, y_work, n_tokens: int | None = None, stream=None) -> None:
@@ -655,7 +504,10 @@ def block_stack_forward(layers, blocks, x, y_work, n_tokens: int | None = None, 
     fp32 x [n_tokens][H]; y_work: fp32 scratch of x's size; blocks: a Block for each layer."""
     if len(blocks) != len(layers):
         raise ValueError("one Block for each layer")
-    dev = _device_of(x, "x")
+    _fp32(x, "x", tuple(getattr(x, "shape", ())), None)
+    if len(x.shape) != 2:
+        raise ValueError("x must be a matrix")
+    dev = x.get_device()
     T = x.shape[0] if n_tokens is None else n_tokens
     if not 0 <= T <= x.shape[0]:
         raise ValueError("n_tokens must be in [0, x.shape[0]]")
@@ -663,15 +515,15 @@ def block_stack_forward(layers, blocks, x, y_work, n_tokens: int | None = None, 
     for l, b in zip(layers, blocks):
         if l.device != dev or l.cfg.hidden != H:
             raise ValueError("the layers must have x's device and width")
-        _blocks(b, None, H, dev)
-    for t, name in ((x, "x"), (y_work, "y_work")):
-        _arr(t, name, tuple(x.shape), _torch().float32, dev)
+        if b.device is not None and (b.device != dev or b.hidden != H):
+            raise ValueError(f"a block's arrays are not [{H}] on cuda:{dev}")
+    _fp32(y_work, "y_work", tuple(x.shape), dev)
     arr = (ctypes.c_void_p * len(layers))(*[l.handle.value for l in layers])
     par = (Block * len(blocks))()
     for i, b in enumerate(blocks):
         ctypes.memmove(ctypes.addressof(par) + i * ctypes.sizeof(Block), b.address, ctypes.sizeof(Block))
     _check(lib.coli_moe_block_stack_forward(ctypes.cast(arr, ctypes.c_void_p), ctypes.cast(par, ctypes.c_void_p),
-                                            len(layers), _ptr(x), _ptr(y_work), T, _stream_on(stream, dev)),
+                                            len(layers), _ptr(x), _ptr(y_work), T, _stream(stream, dev)),
            "coli_moe_block_stack_forward")
 
 

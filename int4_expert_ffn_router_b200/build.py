@@ -7,6 +7,7 @@ import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 SO = os.path.join(HERE, "libcoli_moe.so")
+BINDING_SO = os.path.join(HERE, "_binding.so")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
@@ -25,7 +26,28 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     if verbose:
         print(" ".join(cmd))
     subprocess.check_call(cmd)
+    build_binding(verbose)
     return SO
+
+
+def build_binding(verbose: bool = False) -> str:
+    """The Python module of the operators on torch tensors (csrc/binding.cpp), linked to libcoli_moe.so beside it."""
+    import importlib.util
+    import sysconfig
+
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(torch, "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           *(x for i in inc for x in ("-isystem", i)),
+           os.path.join(HERE, "csrc", "binding.cpp"), "-o", BINDING_SO, SO, "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch",
+           "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.check_call(cmd)
+    return BINDING_SO
 
 
 if __name__ == "__main__":
