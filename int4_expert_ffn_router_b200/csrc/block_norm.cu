@@ -23,8 +23,8 @@ struct NormArgs {
     void *dx, *dy;
     int64_t lddx, lddy;
     float *dtoken;
-    float *part;            // [grid][3][H] partial sums of dpre, dpost, dgate
-    int want;               // bit 0: dpre, bit 1: dpost, bit 2: dgate
+    float* part;            // [grid][2][H] the blocks' sums over their rows of s r dn and of u y rho ds (NULL: not wanted)
+    int stages;             // slots of the ring in shared memory (0: none)
 };
 
 // A sum of squares that fp32 holds well: it neither overflowed nor lost to
@@ -47,112 +47,248 @@ __device__ __forceinline__ void load_gain(const float* g, int c, float (&v)[V]) 
 }
 
 // ---------------------------------------------------------------------------
-// Forward, one block a row. A thread's N x V columns of x and y stay in
-// registers between the two sums.
+// The kernels keep a thread's N x V columns of a row in registers. A block
+// takes the rows b, b + grid, ...: the columns' parameters are read once, and
+// with 16-byte accesses (V = 8) the next rows are copied into a ring in shared
+// memory (cp.async) while a row is worked on. A thread copies what it alone
+// reads, so the ring needs no barrier.
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits for the oldest of the groups in flight (stages - 1 of them, or one).
+__device__ __forceinline__ void cp_async_wait(int stages) {
+    if (stages >= 4) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (stages == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// 16-byte pieces of V = 8 columns; a piece of every thread lies side by side.
+template <typename T>
+constexpr int kPieces = sizeof(T) / 2;
+template <typename T, int N>
+__device__ __forceinline__ uint32_t ring_bytes() { return (uint32_t)(N * kPieces<T> * blockDim.x * 16); }
+
+template <typename T, int N>
+__device__ __forceinline__ void ring_copy(uint32_t dst, const T* row, int H) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * 8;
+        if (c < H)
+#pragma unroll
+            for (int j = 0; j < kPieces<T>; ++j)
+                cp_async16(dst + ((i * kPieces<T> + j) * blockDim.x + threadIdx.x) * 16,
+                           reinterpret_cast<const char*>(row + c) + 16 * j);
+    }
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+    return r;
+}
+// This thread's piece i of a row: from its ring slot (V = 8), or from memory.
+template <typename T, int V>
+__device__ __forceinline__ void take(Raw<T, V>& r, bool on, int i, uint32_t slot, const T* row, int H) {
+    const int c = (i * blockDim.x + threadIdx.x) * V;
+    r.zero();
+    if (!on || c >= H) return;
+    if constexpr (V == 8) {
+        const uint32_t at = slot + (i * kPieces<T> * blockDim.x + threadIdx.x) * 16;
+        r.a = lds16(at);
+        if constexpr (kPieces<T> == 2) r.b = lds16(at + blockDim.x * 16);
+    } else {
+        r.load(row + c);
+    }
+}
+
+// Sums over the block of NR <= 8 values, in every thread, in a fixed order. A
+// warp first halves what a lane holds with every exchange (9 shuffles for 8
+// values), then every warp adds the warps' sums. `red`: 32 * 8 floats, two of
+// them in turn (one barrier a call).
+template <int NR>
+__device__ __forceinline__ void block_sums(float (&v)[NR], float* red) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    constexpr int P = NR <= 1 ? 1 : NR <= 2 ? 2 : NR <= 4 ? 4 : 8;
+    float w[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) w[j] = j < NR ? v[j] : 0.0f;
+    int o = 16;
+#pragma unroll
+    for (int half = P / 2; half >= 1; half /= 2) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int j = 0; j < half; ++j) {
+            const float keep = up ? w[j + half] : w[j], send = up ? w[j] : w[j + half];
+            w[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+        o /= 2;
+    }
+    constexpr int kLast = 16 / P;  // the lanes that hold one value: 32 / P neighbours
+#pragma unroll
+    for (int q = kLast; q >= 1; q /= 2) w[0] += __shfl_xor_sync(0xffffffffu, w[0], q);
+    if (lane % (32 / P) == 0) red[warp * P + lane / (32 / P)] = w[0];
+    __syncthreads();
+    float t = 0.0f;
+    for (int i = lane / P; i < nw; i += 32 / P) t += red[i * P + lane % P];
+#pragma unroll
+    for (int q = P; q < 32; q *= 2) t += __shfl_xor_sync(0xffffffffu, t, q);
+#pragma unroll
+    for (int j = 0; j < NR; ++j) v[j] = __shfl_sync(0xffffffffu, t, j);
+}
+
+// The branch's factor of each column: y_scale * gate * post_gain.
+template <int V>
+__device__ __forceinline__ void load_branch(const NormArgs& a, int c, float (&b)[V]) {
+    float p[V];
+    load_gain<V>(a.gate, c, b);
+    load_gain<V>(a.post, c, p);
+#pragma unroll
+    for (int j = 0; j < V; ++j) b[j] *= a.ys * p[j];
+}
+
 template <typename XT, typename YT, typename NT, int V, int N>
-__global__ void __launch_bounds__(1024) block_norm_kernel(NormArgs a) {
-    __shared__ float red[2][32];
+__global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
+    __shared__ float red[2][32 * 8];
     __shared__ double red64[2][32];
-    const int t = blockIdx.x, H = a.H;
-    const XT* x = (const XT*)a.x + (size_t)t * a.ldx;
-    const YT* y = (const YT*)a.y + (size_t)t * a.ldy;
-    float s[N * V];
-    Raw<XT, V> rx[N];
-    Raw<YT, V> ry[N];
+    extern __shared__ __align__(16) unsigned char ring_mem[];
+    const int H = a.H, stages = a.stages;
+    const uint32_t ring = smem_addr(ring_mem);
+    const uint32_t xb = V == 8 ? ring_bytes<XT, N>() : 0, yb = V == 8 && a.has_prev ? ring_bytes<YT, N>() : 0;
+    const XT* x = (const XT*)a.x;
+    const YT* y = (const YT*)a.y;
+    auto prefetch = [&](int t, int slot) {
+        if constexpr (V == 8) {
+            if (t < a.T) {
+                ring_copy<XT, N>(ring + slot * (xb + yb), x + (size_t)t * a.ldx, H);
+                if (a.has_prev) ring_copy<YT, N>(ring + slot * (xb + yb) + xb, y + (size_t)t * a.ldy, H);
+            }
+            cp_async_commit();
+        }
+    };
+    for (int i = 0; i < stages - 1; ++i) prefetch(blockIdx.x + i * gridDim.x, i);
+    if (stages == 1) prefetch(blockIdx.x, 0);
+    float b[N * V], q[N * V];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * V;
-        rx[i].zero();
-        ry[i].zero();
-        if (c < H) {
-            rx[i].load(x + c);
-            if (a.has_prev) ry[i].load(y + c);
-        }
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = 0.0f;
+        if (a.has_prev && c < H) load_branch<V>(a, c, f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) b[i * V + j] = f[j];
+        if (a.has_next && c < H) load_gain<V>(a.pre, c, f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) q[i * V + j] = f[j];
     }
-    float scale = 1.0f;
-    if (a.has_prev) {
-        scale = a.ys * (a.token ? a.token[t] : 1.0f);
-        float rho = 1.0f;
-        if (a.post_norm) {
-            float ss[1] = {0.0f};
+    int slot = 0;
+    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+        Raw<XT, V> rx[N];
+        Raw<YT, V> ry[N];
+        if constexpr (V == 8) {
+            cp_async_wait(stages);
+            // into the slot of the row before this one, which this thread has read
+            if (stages > 1) prefetch(t + (stages - 1) * gridDim.x, slot == 0 ? stages - 1 : slot - 1);
+        }
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                float v[V];
-                ry[i].get(v);
-#pragma unroll
-                for (int j = 0; j < V; ++j) ss[0] = fmaf(v[j], v[j], ss[0]);
-            }
-            block_sum<float, 1>(ss, red[0]);
-            rho = rms_scale(ss[0], H, a.eps_post);
-            if (!sum_ok(ss[0], a.eps_post)) {
-                double dd[1] = {0.0};
+        for (int i = 0; i < N; ++i) {
+            take<XT, V>(rx[i], true, i, ring + slot * (xb + yb), x + (size_t)t * a.ldx, H);
+            take<YT, V>(ry[i], a.has_prev, i, ring + slot * (xb + yb) + xb, y + (size_t)t * a.ldy, H);
+        }
+        if (stages == 1) prefetch(t + gridDim.x, 0);
+        slot = slot + 1 >= stages ? 0 : slot + 1;
+        float ss[1] = {0.0f};
+        if (a.has_prev) {
+            float scale = a.token ? a.token[t] : 1.0f;
+            if (a.post_norm) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
                     float v[V];
                     ry[i].get(v);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) dd[0] += (double)v[j] * v[j];
+                    for (int j = 0; j < V; ++j) ss[0] = fmaf(v[j], v[j], ss[0]);
                 }
-                block_sum<double, 1>(dd, red64[0]);
-                rho = rms_scale(dd[0], H, a.eps_post);
+                block_sums<1>(ss, red[0]);
+                float rho = rms_scale(ss[0], H, a.eps_post);
+                if (!sum_ok(ss[0], a.eps_post)) {
+                    double dd[1] = {0.0};
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        float v[V];
+                        ry[i].get(v);
+#pragma unroll
+                        for (int j = 0; j < V; ++j) dd[0] += (double)v[j] * v[j];
+                    }
+                    block_sum<double, 1>(dd, red64[0]);
+                    rho = rms_scale(dd[0], H, a.eps_post);
+                }
+#pragma unroll
+                for (int i = 0; i < N; ++i) {  // y rho first: a row of large values times a small gate stays finite
+                    float vx[V], vy[V];
+                    rx[i].get(vx);
+                    ry[i].get(vy);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) vx[j] = fmaf(scale * b[i * V + j], vy[j] * rho, a.xs * vx[j]);
+                    rx[i].set(vx);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    float vx[V], vy[V];
+                    rx[i].get(vx);
+                    ry[i].get(vy);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) vx[j] = fmaf(scale * b[i * V + j], vy[j], a.xs * vx[j]);
+                    rx[i].set(vx);
+                }
             }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int c = (i * blockDim.x + threadIdx.x) * V;
+                if (c < H) rx[i].store((XT*)a.xo + (size_t)t * a.ldxo + c);
+                else rx[i].zero();
+            }
+        }
+        if (!a.has_next) {
+            if (a.post_norm) __syncthreads();  // the next row's sum reuses red[0]
+            continue;
+        }
+        ss[0] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float v[V];
+            rx[i].get(v);  // as stored: what a later read of x_out sees
+#pragma unroll
+            for (int j = 0; j < V; ++j) ss[0] = fmaf(v[j], v[j], ss[0]);
+        }
+        block_sums<1>(ss, red[1]);
+        float r = rms_scale(ss[0], H, a.eps_pre);
+        if (!sum_ok(ss[0], a.eps_pre)) {
+            double dd[1] = {0.0};
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float v[V];
+                rx[i].get(v);
+#pragma unroll
+                for (int j = 0; j < V; ++j) dd[0] += (double)v[j] * v[j];
+            }
+            block_sum<double, 1>(dd, red64[1]);
+            r = rms_scale(dd[0], H, a.eps_pre);
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * V;
-            if (c >= H) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) s[i * V + j] = 0.0f;
-                continue;
-            }
-            float vx[V], vy[V], p[V], g[V];
-            rx[i].get(vx);
-            ry[i].get(vy);
-            load_gain<V>(a.post, c, p);
-            load_gain<V>(a.gate, c, g);
-            float o[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) o[j] = fmaf(scale * g[j], vy[j] * rho * p[j], a.xs * vx[j]);
-            rx[i].set(o);
-            rx[i].store((XT*)a.xo + (size_t)t * a.ldxo + c);
-            rx[i].get(vx);  // as stored: what a later read of x_out sees
-#pragma unroll
-            for (int j = 0; j < V; ++j) s[i * V + j] = vx[j];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
+            if (c >= H) continue;
             float v[V];
             rx[i].get(v);
 #pragma unroll
-            for (int j = 0; j < V; ++j) s[i * V + j] = v[j];
+            for (int j = 0; j < V; ++j) v[j] = v[j] * r * q[i * V + j];
+            Raw<NT, V> out;
+            out.set(v);
+            out.store((NT*)a.n + (size_t)t * a.ldn + c);
         }
-    }
-    if (!a.has_next) return;
-    float ss[1] = {0.0f};
-#pragma unroll
-    for (int i = 0; i < N * V; ++i) ss[0] = fmaf(s[i], s[i], ss[0]);
-    block_sum<float, 1>(ss, red[1]);
-    float r = rms_scale(ss[0], H, a.eps_pre);
-    if (!sum_ok(ss[0], a.eps_pre)) {
-        double dd[1] = {0.0};
-#pragma unroll
-        for (int i = 0; i < N * V; ++i) dd[0] += (double)s[i] * s[i];
-        block_sum<double, 1>(dd, red64[1]);
-        r = rms_scale(dd[0], H, a.eps_pre);
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
-        if (c >= H) continue;
-        float q[V], o[V];
-        load_gain<V>(a.pre, c, q);
-#pragma unroll
-        for (int j = 0; j < V; ++j) o[j] = s[i * V + j] * r * q[j];
-        Raw<NT, V> out;
-        out.set(o);
-        out.store((NT*)a.n + (size_t)t * a.ldn + c);
+        if (!a.has_prev || !a.post_norm) __syncthreads();  // the next row's sum reuses red[1]
     }
 }
 
@@ -249,168 +385,194 @@ __global__ void __launch_bounds__(1024) block_norm_wide_kernel(NormArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Backward. With sh = s r and yh = y rho (the normalised rows):
-//   ds = dxo + r (q dn - sh mean(sh q dn))      dx = xs ds      dq = sum_t sh dn
-//   dz = ys u g ds (z = yh p)                   dg = sum_t ys u z ds, du = sum_c ys g z ds
-//   dy = rho (p dz - yh mean(yh p dz))          dp = sum_t yh dz
-// Two rounds of sums a row: {s^2, s q dn, y^2}, then {y p dz, ys g z ds}. A block
-// takes the rows b, b + grid, ... and keeps the sums over its rows of its
-// threads' columns (dq, dp, dg) in registers; sum_parts_kernel adds the blocks'.
+// Backward. With sh = s r and yh = y rho (the normalised rows), b = ys g p:
+//   ds = dxo + r (q dn - sh m1), m1 = mean(sh q dn)      dx = xs ds      dq = sum_t sh dn
+//   dy = rho (u b ds - yh m2),   m2 = mean(yh u b ds)    du = sum_c b yh ds
+//   A  = sum_t u yh ds, of which dp = ys g A and dg = ys p A
+// m2 and du need ds only in sums, and ds is linear in three of them, so one
+// round of six sums a row is enough:
+//   s^2, s q dn, y^2, b y dxo, b y q dn, b y s:   sum b yh ds = rho (S3 + r (S4 - r m1 S5)).
+// A block keeps dq and A of its threads' columns over its rows in registers;
+// sum_parts_kernel adds the blocks'.
 // ---------------------------------------------------------------------------
 template <typename XT, typename YT, typename NT, int V, int N>
-__global__ void __launch_bounds__(1024) block_norm_backward_kernel(NormArgs a) {
-    __shared__ float red[2][32 * 3];
-    __shared__ double red64[2][32 * 3];
-    const int H = a.H;
-    float dq[N * V], dp[N * V], dg[N * V];
+__global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs a) {
+    __shared__ float red[2][32 * 8];
+    __shared__ double red64[32 * 6];
+    extern __shared__ __align__(16) unsigned char ring_mem[];
+    const int H = a.H, stages = a.stages;
+    const uint32_t ring = smem_addr(ring_mem);
+    const bool has_o = a.dxo != nullptr;
+    uint32_t yo = 0, oo = 0, no = 0, slot_bytes = 0;  // offsets of y, dxo and dn in a slot
+    if constexpr (V == 8) {
+        yo = ring_bytes<XT, N>();
+        oo = yo + (a.has_prev ? ring_bytes<YT, N>() : 0);
+        no = oo + (has_o ? ring_bytes<XT, N>() : 0);
+        slot_bytes = no + (a.has_next ? ring_bytes<NT, N>() : 0);
+    }
+    const XT *s_ = (const XT*)a.x, *o_ = (const XT*)a.dxo;
+    const YT* y_ = (const YT*)a.y;
+    const NT* n_ = (const NT*)a.dn;
+    auto prefetch = [&](int t, int slot) {
+        if constexpr (V == 8) {
+            if (t < a.T) {
+                const uint32_t at = ring + slot * slot_bytes;
+                ring_copy<XT, N>(at, s_ + (size_t)t * a.ldx, H);
+                if (a.has_prev) ring_copy<YT, N>(at + yo, y_ + (size_t)t * a.ldy, H);
+                if (has_o) ring_copy<XT, N>(at + oo, o_ + (size_t)t * a.lddxo, H);
+                if (a.has_next) ring_copy<NT, N>(at + no, n_ + (size_t)t * a.lddn, H);
+            }
+            cp_async_commit();
+        }
+    };
+    for (int i = 0; i < stages - 1; ++i) prefetch(blockIdx.x + i * gridDim.x, i);
+    if (stages == 1) prefetch(blockIdx.x, 0);
+    float b[N * V], q[N * V], dq[N * V], A[N * V];
 #pragma unroll
-    for (int i = 0; i < N * V; ++i) dq[i] = dp[i] = dg[i] = 0.0f;
+    for (int i = 0; i < N; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * V;
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = 0.0f;
+        if (a.has_prev && c < H) load_branch<V>(a, c, f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) b[i * V + j] = f[j];
+        if (a.has_next && c < H) load_gain<V>(a.pre, c, f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) q[i * V + j] = f[j], dq[i * V + j] = A[i * V + j] = 0.0f;
+    }
+    int slot = 0, flip = 0;
+    const float inv = 1.0f / (float)H;
     for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-        Raw<XT, V> rs[N], ro[N];
-        Raw<YT, V> ry[N];
-        Raw<NT, V> rn[N];
+        if constexpr (V == 8) {
+            cp_async_wait(stages);
+            if (stages > 1) prefetch(t + (stages - 1) * gridDim.x, slot == 0 ? stages - 1 : slot - 1);
+        }
+        const uint32_t at = ring + slot * slot_bytes;
+        slot = slot + 1 >= stages ? 0 : slot + 1;
+        // Wide pieces are read from the ring in every pass over the row; single columns stay in registers.
+        constexpr int kKept = V == 8 ? 1 : N;
+        Raw<XT, V> rs[kKept], ro[kKept];
+        Raw<YT, V> ry[kKept];
+        Raw<NT, V> rn[kKept];
+        auto row = [&](int i, int pass, float (&s)[V], float (&y)[V], float (&o)[V], float (&n)[V]) {
+            const int k = V == 8 ? 0 : i;
+            if (V == 8 || pass == 0) {
+                take<XT, V>(rs[k], true, i, at, s_ + (size_t)t * a.ldx, H);
+                take<YT, V>(ry[k], a.has_prev, i, at + yo, y_ + (size_t)t * a.ldy, H);
+                take<XT, V>(ro[k], has_o, i, at + oo, o_ + (size_t)t * a.lddxo, H);
+                take<NT, V>(rn[k], a.has_next, i, at + no, n_ + (size_t)t * a.lddn, H);
+            }
+            rs[k].get(s);
+            ry[k].get(y);
+            ro[k].get(o);
+            rn[k].get(n);
+        };
+        const float u = a.token ? a.token[t] : 1.0f;
+        float v[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * V;
-            rs[i].zero();
-            ro[i].zero();
-            ry[i].zero();
-            rn[i].zero();
-            if (c < H) {
-                rs[i].load((const XT*)a.x + (size_t)t * a.ldx + c);
-                if (a.has_prev) ry[i].load((const YT*)a.y + (size_t)t * a.ldy + c);
-                if (a.dxo) ro[i].load((const XT*)a.dxo + (size_t)t * a.lddxo + c);
-                if (a.has_next) rn[i].load((const NT*)a.dn + (size_t)t * a.lddn + c);
+            float s[V], n[V], y[V], o[V];
+            row(i, 0, s, y, o, n);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float qn = q[i * V + j] * n[j], by = b[i * V + j] * y[j];
+                v[0] = fmaf(s[j], s[j], v[0]);
+                v[1] = fmaf(s[j], qn, v[1]);
+                v[2] = fmaf(y[j], y[j], v[2]);
+                v[3] = fmaf(by, o[j], v[3]);
+                v[4] = fmaf(by, qn, v[4]);
+                v[5] = fmaf(by, s[j], v[5]);
             }
         }
-        const float u = a.token ? a.token[t] : 1.0f;
-        float r = 0.0f, m1 = 0.0f, rho = 1.0f;
-        {
-            float v[3] = {0.0f, 0.0f, 0.0f};
+        block_sums<6>(v, red[flip]);
+        flip ^= 1;
+        float r = 0.0f, m1 = 0.0f, rho = 1.0f, du;
+        bool ok = (!a.has_next || sum_ok(v[0], a.eps_pre)) && (!a.post_norm || sum_ok(v[2], a.eps_post));
+#pragma unroll
+        for (int j = 0; j < 6; ++j) ok = ok && fabsf(v[j]) <= 3e37f;
+        if (ok) {
+            if (a.has_next) {
+                r = rms_scale(v[0], H, a.eps_pre);
+                m1 = v[1] * r * inv;
+            }
+            if (a.post_norm) rho = rms_scale(v[2], H, a.eps_post);
+            du = rho * fmaf(r, fmaf(-r * m1, v[5], v[4]), v[3]);
+        } else {  // a row beyond fp32's range (or not finite): the same sums in fp64
+            double w[6] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int c = (i * blockDim.x + threadIdx.x) * V;
-                if (c >= H) continue;
-                float s[V], n[V], y[V], q[V];
-                rs[i].get(s);
-                rn[i].get(n);
-                ry[i].get(y);
-                load_gain<V>(a.pre, c, q);
+                float s[V], n[V], y[V], o[V];
+                row(i, 1, s, y, o, n);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    v[0] = fmaf(s[j], s[j], v[0]);
-                    v[1] = fmaf(s[j], q[j] * n[j], v[1]);
-                    v[2] = fmaf(y[j], y[j], v[2]);
+                    const double qn = (double)q[i * V + j] * n[j], by = (double)b[i * V + j] * y[j];
+                    w[0] += (double)s[j] * s[j];
+                    w[1] += s[j] * qn;
+                    w[2] += (double)y[j] * y[j];
+                    w[3] += by * o[j];
+                    w[4] += by * qn;
+                    w[5] += by * s[j];
                 }
             }
-            block_sum<float, 3>(v, red[0]);
-            const bool ok = (!a.has_next || sum_ok(v[0], a.eps_pre)) && (!a.post_norm || sum_ok(v[2], a.eps_post));
-            if (ok) {
-                r = rms_scale(v[0], H, a.eps_pre);
-                m1 = v[1] * r / (float)H;
-                if (a.post_norm) rho = rms_scale(v[2], H, a.eps_post);
-            } else {
-                double w[3] = {0.0, 0.0, 0.0};
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int c = (i * blockDim.x + threadIdx.x) * V;
-                    if (c >= H) continue;
-                    float s[V], n[V], y[V], q[V];
-                    rs[i].get(s);
-                    rn[i].get(n);
-                    ry[i].get(y);
-                    load_gain<V>(a.pre, c, q);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        w[0] += (double)s[j] * s[j];
-                        w[1] += (double)s[j] * q[j] * n[j];
-                        w[2] += (double)y[j] * y[j];
-                    }
-                }
-                block_sum<double, 3>(w, red64[0]);
-                r = rms_scale(w[0], H, a.eps_pre);
-                m1 = (float)(w[1] * (double)r / H);
-                if (a.post_norm) rho = rms_scale(w[2], H, a.eps_post);
+            block_sum<double, 6>(w, red64);
+            __syncthreads();  // the next such row reuses red64
+            double rd = 0.0, md = 0.0, pd = 1.0;
+            if (a.has_next) {
+                rd = 1.0 / sqrt(w[0] / H + (double)a.eps_pre);
+                md = w[1] * rd / H;
             }
+            if (a.post_norm) pd = 1.0 / sqrt(w[2] / H + (double)a.eps_post);
+            r = (float)rd;
+            m1 = (float)md;
+            rho = (float)pd;
+            du = (float)(pd * (w[3] + rd * (w[4] - rd * md * w[5])));
         }
-        float ds[N * V];
-        float v[2] = {0.0f, 0.0f};  // sum of yh p dz, of ys g z ds
+        if (a.dtoken && threadIdx.x == 0) a.dtoken[t] = du;
+        const float m2 = a.post_norm ? u * du * inv : 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * V;
+            float s[V], n[V], y[V], o[V];
+            row(i, 1, s, y, o, n);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int k = i * V + j;
+                const float sh = s[j] * r, yh = y[j] * rho;
+                dq[k] = fmaf(sh, n[j], dq[k]);
+                o[j] = fmaf(r, fmaf(-sh, m1, q[k] * n[j]), o[j]);
+                A[k] = fmaf(u * yh, o[j], A[k]);
+                y[j] = rho * fmaf(-yh, m2, u * b[k] * o[j]);
+                o[j] *= a.xs;
+            }
             if (c >= H) continue;
-            float s[V], n[V], y[V], o[V], q[V], p[V], g[V];
-            ro[i].get(o);
-            if (a.has_next) {
-                rs[i].get(s);
-                rn[i].get(n);
-                load_gain<V>(a.pre, c, q);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float sh = s[j] * r;
-                    dq[i * V + j] = fmaf(sh, n[j], dq[i * V + j]);
-                    o[j] = fmaf(r, fmaf(-sh, m1, q[j] * n[j]), o[j]);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < V; ++j) ds[i * V + j] = o[j];
-            if (a.has_prev) {
-                ry[i].get(y);
-                load_gain<V>(a.post, c, p);
-                load_gain<V>(a.gate, c, g);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float yh = y[j] * rho, zd = a.ys * yh * p[j] * o[j], dz = a.ys * u * g[j] * o[j];
-                    dp[i * V + j] = fmaf(yh, dz, dp[i * V + j]);
-                    dg[i * V + j] = fmaf(u, zd, dg[i * V + j]);
-                    v[0] = fmaf(yh, p[j] * dz, v[0]);
-                    v[1] = fmaf(g[j], zd, v[1]);
-                    o[j] *= a.xs;
-                }
-            }
             if (a.dx) {
                 Raw<XT, V> out;
                 out.set(o);
                 out.store((XT*)a.dx + (size_t)t * a.lddx + c);
             }
+            if (a.dy) {
+                Raw<YT, V> out;
+                out.set(y);
+                out.store((YT*)a.dy + (size_t)t * a.lddy + c);
+            }
         }
-        if (!a.has_prev) {
-            __syncthreads();  // the next row's sums reuse red[0]
-            continue;
-        }
-        block_sum<float, 2>(v, red[1]);
-        if (a.dtoken && threadIdx.x == 0) a.dtoken[t] = v[1];
-        if (!a.dy) continue;
-        const float m2 = a.post_norm ? v[0] / (float)H : 0.0f;
+        if (stages == 1) prefetch(t + gridDim.x, 0);
+    }
+    if (a.part) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * V;
             if (c >= H) continue;
-            float y[V], p[V], g[V];
-            ry[i].get(y);
-            load_gain<V>(a.post, c, p);
-            load_gain<V>(a.gate, c, g);
+            float* out = a.part + (size_t)blockIdx.x * 2 * H + c;
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                y[j] = rho * fmaf(-(y[j] * rho), m2, p[j] * (a.ys * u * g[j] * ds[i * V + j]));
-            Raw<YT, V> out;
-            out.set(y);
-            out.store((YT*)a.dy + (size_t)t * a.lddy + c);
+            for (int j = 0; j < V; ++j) {
+                out[j] = dq[i * V + j];
+                out[(size_t)H + j] = A[i * V + j];
+            }
         }
     }
-    if (!a.want) return;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
-        if (c >= H) continue;
-        float* out = a.part + (size_t)blockIdx.x * 3 * H + c;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            if (a.want & 1) out[j] = dq[i * V + j];
-            if (a.want & 2) out[(size_t)H + j] = dp[i * V + j];
-            if (a.want & 4) out[(size_t)2 * H + j] = dg[i * V + j];
-        }
-    }
+    grid_next();
 }
 
 // Rows too wide for registers: the columns are read again in each round, and
@@ -419,7 +581,7 @@ template <typename XT, typename YT, typename NT>
 __global__ void __launch_bounds__(1024) block_norm_backward_wide_kernel(NormArgs a) {
     __shared__ double red64[2][32 * 3];
     const int H = a.H;
-    float* part = a.want ? a.part + (size_t)blockIdx.x * 3 * H : nullptr;
+    float* part = a.part ? a.part + (size_t)blockIdx.x * 2 * H : nullptr;
     for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
         const float u = a.token ? a.token[t] : 1.0f;
         const bool first = t == (int)blockIdx.x;
@@ -461,33 +623,32 @@ __global__ void __launch_bounds__(1024) block_norm_backward_wide_kernel(NormArgs
         const float r = rms_scale(w[0], H, a.eps_pre);
         const float m1 = (float)(w[1] * (double)r / H);
         const float rho = a.post_norm ? rms_scale(w[2], H, a.eps_post) : 1.0f;
-        double v[2] = {0.0, 0.0};
+        double v[1] = {0.0};
         float m2 = 0.0f;
         for (int round = 0; round < 2; ++round) {
             for (int c = threadIdx.x; c < H; c += blockDim.x) {
-                float s, y, n, o, q[1], p[1], g[1];
+                float s, y, n, o, q[1], b[1] = {0.0f};
                 row(c, s, y, n, o);
                 load_gain<1>(a.pre, c, q);
-                load_gain<1>(a.post, c, p);
-                load_gain<1>(a.gate, c, g);
+                if (a.has_prev) load_branch<1>(a, c, b);
                 const float sh = s * r;
                 if (a.has_next) o = fmaf(r, fmaf(-sh, m1, q[0] * n), o);
-                const float yh = y * rho, zd = a.ys * yh * p[0] * o, dz = a.ys * u * g[0] * o;
+                const float yh = y * rho;
                 if (round == 0) {
-                    v[0] += (double)yh * p[0] * dz;
-                    v[1] += (double)g[0] * zd;
-                    if (a.want & 1) part[c] = first ? sh * n : fmaf(sh, n, part[c]);
-                    if (a.want & 2) part[H + c] = first ? yh * dz : fmaf(yh, dz, part[H + c]);
-                    if (a.want & 4) part[2 * H + c] = first ? u * zd : fmaf(u, zd, part[2 * H + c]);
+                    v[0] += (double)b[0] * yh * o;
+                    if (part) {
+                        part[c] = first ? sh * n : fmaf(sh, n, part[c]);
+                        part[H + c] = first ? u * yh * o : fmaf(u * yh, o, part[H + c]);
+                    }
                 } else {  // every input of this column has been read: dx and dy may be inputs
-                    float f[1] = {a.has_prev ? a.xs * o : o};
+                    float f[1] = {a.xs * o};
                     if (a.dx) {
                         Raw<XT, 1> out;
                         out.set(f);
                         out.store((XT*)a.dx + (size_t)t * a.lddx + c);
                     }
                     if (a.dy) {
-                        f[0] = rho * fmaf(-yh, m2, p[0] * dz);
+                        f[0] = rho * fmaf(-yh, m2, u * b[0] * o);
                         Raw<YT, 1> out;
                         out.set(f);
                         out.store((YT*)a.dy + (size_t)t * a.lddy + c);
@@ -495,82 +656,112 @@ __global__ void __launch_bounds__(1024) block_norm_backward_wide_kernel(NormArgs
                 }
             }
             if (round == 0) {
-                block_sum<double, 2>(v, red64[1]);
-                if (a.dtoken && threadIdx.x == 0) a.dtoken[t] = (float)v[1];
-                m2 = a.post_norm ? (float)(v[0] / H) : 0.0f;
+                block_sum<double, 1>(v, red64[1]);
+                if (a.dtoken && threadIdx.x == 0) a.dtoken[t] = (float)v[0];
+                m2 = a.post_norm ? (float)(u * v[0] / H) : 0.0f;
             }
         }
     }
 }
 
-// out[k][c] = sum over the blocks of part[b][k][c], in block order: 32 columns
-// and 8 runs of blocks a block.
-__global__ void __launch_bounds__(256) sum_parts_kernel(const float* part, int n, int H, float* o0, float* o1, float* o2) {
+// The gains' and the gate's gradients from the blocks' sums, added in block
+// order: 32 columns and 8 runs of blocks a block.
+__global__ void __launch_bounds__(256) sum_parts_kernel(const NormArgs a, int n, float* dpre, float* dpost, float* dgate) {
     __shared__ float sh[8][32];
     grid_wait();
-    const int which = blockIdx.y, c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
-    float* out = which == 0 ? o0 : which == 1 ? o1 : o2;
-    if (!out) return;
+    const int H = a.H, which = blockIdx.y, c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+    if (which == 0 ? !dpre : !dpost && !dgate) return;
     const int per = (n + 7) / 8, b0 = g * per, b1 = min(n, b0 + per);
     float acc = 0.0f;
     if (c < H)
 #pragma unroll 8
-        for (int b = b0; b < b1; ++b) acc += part[((size_t)b * 3 + which) * H + c];
+        for (int b = b0; b < b1; ++b) acc += __ldcg(a.part + ((size_t)b * 2 + which) * H + c);
     sh[g][threadIdx.x & 31] = acc;
     __syncthreads();
-    if (g == 0 && c < H) {
+    if (g != 0 || c >= H) return;
 #pragma unroll
-        for (int i = 1; i < 8; ++i) acc += sh[i][threadIdx.x];
-        out[c] = acc;
+    for (int i = 1; i < 8; ++i) acc += sh[i][threadIdx.x];
+    if (which == 0) {
+        dpre[c] = acc;
+        return;
     }
+    acc *= a.ys;
+    if (dpost) dpost[c] = acc * (a.gate ? a.gate[c] : 1.0f);
+    if (dgate) dgate[c] = acc * (a.post ? a.post[c] : 1.0f);
 }
 
-constexpr int kPartBlocks = 296;  // blocks whose partial sums the workspace holds
-int backward_grid(int T) { return T < kPartBlocks ? T : kPartBlocks; }
-
-// V, N and threads for rows of H columns: 8-column accesses in up to 1024
-// threads; single columns otherwise; N == 0: too wide for registers.
+// V, N and threads for rows of H columns, up to 512 threads; N == 0: too wide
+// for registers.
 struct Shape {
     int V, N, threads;
 };
 Shape shape_of(int H, bool vec) {
     const int V = vec ? 8 : 1;
     const int n = (H + V - 1) / V;
-    for (int N : {1, 2, 8}) {
+    for (int N : {1, 2, 4, 8}) {
         if (vec && N > 2) break;
         const int th = ((n + N - 1) / N + 31) / 32 * 32;
-        if (th <= (vec ? 1024 : 512) || (!vec && N == 8 && th <= 1024)) return {V, N, th};
+        if (th <= 512) return {V, N, th};
     }
-    return {V, 0, 1024};
+    return {V, 0, 512};
+}
+
+constexpr int kSms = 148;
+// Blocks of `threads` that share an SM, and so the grid of a persistent launch.
+int blocks_per_sm(int threads) { return threads >= 512 ? 1 : threads >= 256 ? 2 : threads >= 128 ? 4 : 8; }
+int grid_of(int T, int H) {  // the same for aligned and unaligned rows: the workspace's size depends on it
+    const int vec_threads = shape_of(H, true).threads, threads = H % 8 ? shape_of(H, false).threads : vec_threads;
+    const int g = kSms * blocks_per_sm(threads < vec_threads ? threads : vec_threads);
+    return T < g ? T : g;
+}
+// Ring slots of `row` bytes (at most 128 KB) that fit beside the other blocks of an SM.
+int stages_of(size_t row, int threads, int rows) {
+    const size_t n = 200 * 1024 / blocks_per_sm(threads) / row;
+    return n < 1 || rows < 2 ? 1 : n > 4 ? 4 : (int)n;
 }
 
 using B = __nv_bfloat16;
+using Kernel = void (*)(NormArgs);
 
-template <typename XT, typename YT, typename NT>
-cudaError_t forward_typed(const NormArgs& a, bool vec, cudaStream_t st) {
-    const Shape s = shape_of(a.H, vec);
-    void (*k)(NormArgs) = s.N == 0   ? block_norm_wide_kernel<XT, YT, NT>
-                          : s.V == 8 ? (s.N == 1 ? block_norm_kernel<XT, YT, NT, 8, 1> : block_norm_kernel<XT, YT, NT, 8, 2>)
-                          : s.N == 1 ? block_norm_kernel<XT, YT, NT, 1, 1>
-                          : s.N == 2 ? block_norm_kernel<XT, YT, NT, 1, 2>
-                                     : block_norm_kernel<XT, YT, NT, 1, 8>;
-    return launch(k, a.T, s.threads, 0, st, false, a);
+cudaError_t launch_rows(Kernel k, NormArgs& a, const Shape& s, size_t col_bytes, int grid, cudaStream_t st) {
+    const size_t row = s.V == 8 && s.N ? col_bytes * 8 * s.N * s.threads : 0;
+    a.stages = row ? stages_of(row, s.threads, (a.T + grid - 1) / grid) : 0;
+    const size_t smem = a.stages * row;
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch(k, grid, s.threads, smem, st, false, a);
 }
 
 template <typename XT, typename YT, typename NT>
-cudaError_t backward_typed(const NormArgs& a, bool vec, cudaStream_t st) {
+cudaError_t forward_typed(NormArgs& a, bool vec, cudaStream_t st) {
     const Shape s = shape_of(a.H, vec);
-    void (*k)(NormArgs) = s.N == 0 ? block_norm_backward_wide_kernel<XT, YT, NT>
-                          : s.V == 8
-                              ? (s.N == 1 ? block_norm_backward_kernel<XT, YT, NT, 8, 1> : block_norm_backward_kernel<XT, YT, NT, 8, 2>)
-                          : s.N == 1 ? block_norm_backward_kernel<XT, YT, NT, 1, 1>
-                          : s.N == 2 ? block_norm_backward_kernel<XT, YT, NT, 1, 2>
-                                     : block_norm_backward_kernel<XT, YT, NT, 1, 8>;
-    return launch(k, backward_grid(a.T), s.threads, 0, st, false, a);
+    const Kernel k = s.N == 0   ? block_norm_wide_kernel<XT, YT, NT>
+                     : s.V == 8 ? (s.N == 1 ? block_norm_kernel<XT, YT, NT, 8, 1> : block_norm_kernel<XT, YT, NT, 8, 2>)
+                     : s.N == 1 ? block_norm_kernel<XT, YT, NT, 1, 1>
+                     : s.N == 2 ? block_norm_kernel<XT, YT, NT, 1, 2>
+                     : s.N == 4 ? block_norm_kernel<XT, YT, NT, 1, 4>
+                                : block_norm_kernel<XT, YT, NT, 1, 8>;
+    return launch_rows(k, a, s, sizeof(XT) + (a.has_prev ? sizeof(YT) : 0), s.N ? grid_of(a.T, a.H) : a.T, st);
+}
+
+template <typename XT, typename YT, typename NT>
+cudaError_t backward_typed(NormArgs& a, bool vec, cudaStream_t st) {
+    const Shape s = shape_of(a.H, vec);
+    const Kernel k = s.N == 0 ? block_norm_backward_wide_kernel<XT, YT, NT>
+                     : s.V == 8
+                         ? (s.N == 1 ? block_norm_backward_kernel<XT, YT, NT, 8, 1> : block_norm_backward_kernel<XT, YT, NT, 8, 2>)
+                     : s.N == 1 ? block_norm_backward_kernel<XT, YT, NT, 1, 1>
+                     : s.N == 2 ? block_norm_backward_kernel<XT, YT, NT, 1, 2>
+                     : s.N == 4 ? block_norm_backward_kernel<XT, YT, NT, 1, 4>
+                                : block_norm_backward_kernel<XT, YT, NT, 1, 8>;
+    const size_t col = sizeof(XT) * (a.dxo ? 2 : 1) + (a.has_prev ? sizeof(YT) : 0) + (a.has_next ? sizeof(NT) : 0);
+    return launch_rows(k, a, s, col, grid_of(a.T, a.H), st);
 }
 
 template <bool fwd>
-cudaError_t by_type(const NormArgs& a, coli_dtype xt, coli_dtype yt, coli_dtype nt, bool vec, cudaStream_t st) {
+cudaError_t by_type(NormArgs& a, coli_dtype xt, coli_dtype yt, coli_dtype nt, bool vec, cudaStream_t st) {
     auto go = [&](auto x, auto y, auto n) {
         if constexpr (fwd) return forward_typed<decltype(x), decltype(y), decltype(n)>(a, vec, st);
         else return backward_typed<decltype(x), decltype(y), decltype(n)>(a, vec, st);
@@ -590,6 +781,7 @@ bool gain_vec(const float* p) { return ((uintptr_t)p & 15u) == 0; }
 void set_params(NormArgs& a, const coli_block_params* prev, const coli_block_params* next) {
     a.has_prev = prev != nullptr;
     a.has_next = next != nullptr;
+    a.xs = 1.0f;
     if (prev) {
         a.post = prev->post_gain;
         a.gate = prev->gate;
@@ -721,7 +913,7 @@ COLI_API coli_status coli_block_norm(const coli_block_params* prev, const coli_b
 
 COLI_API int64_t coli_block_norm_workspace(int T, int H) {
     if (T < 0 || T > kBlockMaxTokens || H < 1 || H > kBlockMaxHidden) return -1;
-    return (int64_t)backward_grid(T) * 3 * H * 4;
+    return (int64_t)grid_of(T, H) * 2 * H * 4;
 }
 
 COLI_API coli_status coli_block_norm_backward(const coli_block_params* prev, const coli_block_params* next,
@@ -743,7 +935,7 @@ COLI_API coli_status coli_block_norm_backward(const coli_block_params* prev, con
     REQUIRE((((uintptr_t)token_gate | (uintptr_t)dpre_gain | (uintptr_t)dpost_gain | (uintptr_t)dgate |
               (uintptr_t)dtoken_gate) & 3u) == 0,
             "gains, gates and their gradients must be 4-byte aligned");
-    const int want = (dpre_gain ? 1 : 0) | (dpost_gain ? 2 : 0) | (dgate ? 4 : 0);
+    const bool want = dpre_gain || dpost_gain || dgate;
     const int64_t need = want ? coli_block_norm_workspace(T, H) : 0;
     REQUIRE(need == 0 || (work && work_bytes >= need), "work is smaller than coli_block_norm_workspace");
     REQUIRE(need == 0 || ((uintptr_t)work & 15u) == 0, "work must be 16-byte aligned");
@@ -797,8 +989,7 @@ COLI_API coli_status coli_block_norm_backward(const coli_block_params* prev, con
     a.dy = dy;
     a.lddy = dy_stride;
     a.dtoken = dtoken_gate;
-    a.part = (float*)work;
-    a.want = want;
+    a.part = want ? (float*)work : nullptr;
     cudaError_t e = cudaSuccess;
     if (T > 0) {
         const bool vec = H % 8 == 0 && ms.vec() && (!prev || my.vec()) && (!next || mn.vec()) && (!dx_out || mo.vec()) &&
@@ -807,7 +998,6 @@ COLI_API coli_status coli_block_norm_backward(const coli_block_params* prev, con
         if (e != cudaSuccess) return block_cuda_fail(e, "block norm backward");
     }
     if (!want) return COLI_OK;
-    e = launch(sum_parts_kernel, dim3((H + 31) / 32, 3), 256, 0, s, false, (const float*)work, backward_grid(T), H,
-               dpre_gain, dpost_gain, dgate);
+    e = launch(sum_parts_kernel, dim3((H + 31) / 32, 2), 256, 0, s, T > 0, a, grid_of(T, H), dpre_gain, dpost_gain, dgate);
     return e == cudaSuccess ? COLI_OK : block_cuda_fail(e, "block norm backward: gains");
 }
