@@ -47,12 +47,87 @@ __device__ __forceinline__ void load_gain(const float* g, int c, float (&v)[V]) 
 }
 
 // ---------------------------------------------------------------------------
-// The kernels keep a thread's N x V columns of a row in registers. A block
-// takes the rows b, b + grid, ...: the columns' parameters are read once, and
-// with 16-byte accesses (V = 8) the next rows are copied into a ring in shared
-// memory (cp.async) while a row is worked on. A thread copies what it alone
-// reads, so the ring needs no barrier.
+// A thread holds N pieces of V columns of a row: V = 8 with 16-byte accesses
+// (rows that start on 16-byte boundaries, H % 8 == 0), else V = 2 read one by
+// one. Arithmetic is on pairs of columns (fp32 x 2 instructions): a row's
+// instructions, not its bytes, bound these kernels otherwise.
+//
+// A block takes the rows b, b + grid, ...: the columns' parameters are read
+// once, and with V = 8 the next rows are copied into a ring in shared memory
+// (cp.async) while a row is worked on. A thread copies what it alone reads, so
+// the ring needs no barrier.
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 bf16_pair(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t to_bf16_pair(float2 v) {
+    const __nv_bfloat162 h = __float22bfloat162_rn(v);  // nearest, ties to even
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename T, int V>
+struct Piece;
+template <>
+struct Piece<float, 8> {
+    uint4 w[2];
+    __device__ __forceinline__ void zero() { w[0] = w[1] = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float2 (&v)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v[2 * i] = make_float2(__uint_as_float(w[i].x), __uint_as_float(w[i].y));
+            v[2 * i + 1] = make_float2(__uint_as_float(w[i].z), __uint_as_float(w[i].w));
+        }
+    }
+    __device__ __forceinline__ void set(const float2 (&v)[4]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = make_uint4(__float_as_uint(v[2 * i].x), __float_as_uint(v[2 * i].y), __float_as_uint(v[2 * i + 1].x),
+                              __float_as_uint(v[2 * i + 1].y));
+    }
+    __device__ __forceinline__ void load(const float* p, int) { w[0] = ld16(p); w[1] = ld16(p + 4); }
+    __device__ __forceinline__ void store(float* p, int) const { st16(p, w[0]); st16(p + 4, w[1]); }
+};
+template <>
+struct Piece<__nv_bfloat16, 8> {
+    uint4 w[1];
+    __device__ __forceinline__ void zero() { w[0] = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float2 (&v)[4]) const {
+        v[0] = bf16_pair(w[0].x); v[1] = bf16_pair(w[0].y); v[2] = bf16_pair(w[0].z); v[3] = bf16_pair(w[0].w);
+    }
+    __device__ __forceinline__ void set(const float2 (&v)[4]) {
+        w[0] = make_uint4(to_bf16_pair(v[0]), to_bf16_pair(v[1]), to_bf16_pair(v[2]), to_bf16_pair(v[3]));
+    }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, int) { w[0] = ld16(p); }
+    __device__ __forceinline__ void store(__nv_bfloat16* p, int) const { st16(p, w[0]); }
+};
+// Two columns, the second of which may lie behind the row's end (left == 1).
+template <typename T>
+struct Piece<T, 2> {
+    Raw<T, 1> a, b;
+    __device__ __forceinline__ void zero() { a.zero(); b.zero(); }
+    __device__ __forceinline__ void get(float2 (&v)[1]) const {
+        float x[1], y[1];
+        a.get(x);
+        b.get(y);
+        v[0] = make_float2(x[0], y[0]);
+    }
+    __device__ __forceinline__ void set(const float2 (&v)[1]) {
+        const float x[1] = {v[0].x}, y[1] = {v[0].y};
+        a.set(x);
+        b.set(y);
+    }
+    __device__ __forceinline__ void load(const T* p, int left) {
+        a.load(p);
+        if (left > 1) b.load(p + 1);
+        else b.zero();
+    }
+    __device__ __forceinline__ void store(T* p, int left) const {
+        a.store(p);
+        if (left > 1) b.store(p + 1);
+    }
+};
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -64,231 +139,260 @@ __device__ __forceinline__ void cp_async_wait(int stages) {
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// 16-byte pieces of V = 8 columns; a piece of every thread lies side by side.
+// 16-byte parts of 8 columns; a part of every thread lies side by side.
 template <typename T>
-constexpr int kPieces = sizeof(T) / 2;
+constexpr int kParts = sizeof(T) / 2;
 template <typename T, int N>
-__device__ __forceinline__ uint32_t ring_bytes() { return (uint32_t)(N * kPieces<T> * blockDim.x * 16); }
+__device__ __forceinline__ uint32_t ring_bytes() { return (uint32_t)(N * kParts<T> * blockDim.x * 16); }
 
+// Copies this thread's pieces of a row (row: its first column's address) to dst (its place in the slot).
 template <typename T, int N>
 __device__ __forceinline__ void ring_copy(uint32_t dst, const T* row, int H) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * 8;
-        if (c < H)
+    for (int i = 0; i < N; ++i)
+        if ((int)(i * blockDim.x + threadIdx.x) * 8 < H)
 #pragma unroll
-            for (int j = 0; j < kPieces<T>; ++j)
-                cp_async16(dst + ((i * kPieces<T> + j) * blockDim.x + threadIdx.x) * 16,
-                           reinterpret_cast<const char*>(row + c) + 16 * j);
-    }
+            for (int j = 0; j < kParts<T>; ++j)
+                cp_async16(dst + (i * kParts<T> + j) * blockDim.x * 16,
+                           reinterpret_cast<const char*>(row + i * blockDim.x * 8) + 16 * j);
 }
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
     uint4 r;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
     return r;
 }
-// This thread's piece i of a row: from its ring slot (V = 8), or from memory.
+// Zeroes this thread's places in the ring that no copy fills: columns behind
+// the row's end, and (all) an array that is absent. Reads then need no conditions.
+template <typename T, int N>
+__device__ __forceinline__ void ring_clear(uint32_t dst, bool all, int H) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (all || (int)(i * blockDim.x + threadIdx.x) * 8 >= H)
+#pragma unroll
+            for (int j = 0; j < kParts<T>; ++j)
+                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + (i * kParts<T> + j) * blockDim.x * 16), "r"(0)
+                             : "memory");
+}
+// This thread's piece i of a row: from its ring slot (V = 8), or from memory (row: its first column's address).
 template <typename T, int V>
-__device__ __forceinline__ void take(Raw<T, V>& r, bool on, int i, uint32_t slot, const T* row, int H) {
-    const int c = (i * blockDim.x + threadIdx.x) * V;
-    r.zero();
-    if (!on || c >= H) return;
+__device__ __forceinline__ void take(Piece<T, V>& r, bool on, int i, uint32_t slot, const T* row, int H) {
     if constexpr (V == 8) {
-        const uint32_t at = slot + (i * kPieces<T> * blockDim.x + threadIdx.x) * 16;
-        r.a = lds16(at);
-        if constexpr (kPieces<T> == 2) r.b = lds16(at + blockDim.x * 16);
+#pragma unroll
+        for (int j = 0; j < kParts<T>; ++j) r.w[j] = lds16(slot + (i * kParts<T> + j) * blockDim.x * 16);
     } else {
-        r.load(row + c);
+        const int left = H - (int)(i * blockDim.x + threadIdx.x) * V;
+        r.zero();
+        if (on && left > 0) r.load(row + i * blockDim.x * V, left);
     }
 }
 
-// Sums over the block of NR <= 8 values, in every thread, in a fixed order. A
-// warp first halves what a lane holds with every exchange (9 shuffles for 8
-// values), then every warp adds the warps' sums. `red`: 32 * 8 floats, two of
-// them in turn (one barrier a call).
+// Sums over the block (at most 16 warps) of NR values, 1 or 5 to 8, in every
+// thread, in a fixed order. `red`: 16 * 8 floats, two of them in turn (one
+// barrier a call).
+__device__ __forceinline__ void block_sums(float (&v)[1], float* red) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 16; o >= 1; o /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    if (lane == 0) red[warp] = v[0];
+    __syncthreads();
+    v[0] = lane < nw ? red[lane] : 0.0f;
+#pragma unroll
+    for (int o = 8; o >= 1; o /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    v[0] = __shfl_sync(0xffffffffu, v[0], 0);
+}
+// With every exchange a lane keeps half of its values (9 shuffles for 8
+// values), then every warp adds the warps' sums, lane l those of value l % 8.
 template <int NR>
 __device__ __forceinline__ void block_sums(float (&v)[NR], float* red) {
+    static_assert(NR > 4 && NR <= 8, "8 values a lane");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    constexpr int P = NR <= 1 ? 1 : NR <= 2 ? 2 : NR <= 4 ? 4 : 8;
-    float w[P];
+    float w[8];
 #pragma unroll
-    for (int j = 0; j < P; ++j) w[j] = j < NR ? v[j] : 0.0f;
-    int o = 16;
+    for (int j = 0; j < 8; ++j) w[j] = j < NR ? v[j] : 0.0f;
 #pragma unroll
-    for (int half = P / 2; half >= 1; half /= 2) {
-        const bool up = lane & o;
+    for (int half = 4; half >= 1; half /= 2) {
+        const bool up = lane & (4 * half);
 #pragma unroll
         for (int j = 0; j < half; ++j) {
             const float keep = up ? w[j + half] : w[j], send = up ? w[j] : w[j + half];
-            w[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            w[j] = keep + __shfl_xor_sync(0xffffffffu, send, 4 * half);
         }
-        o /= 2;
     }
-    constexpr int kLast = 16 / P;  // the lanes that hold one value: 32 / P neighbours
-#pragma unroll
-    for (int q = kLast; q >= 1; q /= 2) w[0] += __shfl_xor_sync(0xffffffffu, w[0], q);
-    if (lane % (32 / P) == 0) red[warp * P + lane / (32 / P)] = w[0];
+    w[0] += __shfl_xor_sync(0xffffffffu, w[0], 2);
+    w[0] += __shfl_xor_sync(0xffffffffu, w[0], 1);
+    if ((lane & 3) == 0) red[warp * 8 + lane / 4] = w[0];
     __syncthreads();
     float t = 0.0f;
-    for (int i = lane / P; i < nw; i += 32 / P) t += red[i * P + lane % P];
 #pragma unroll
-    for (int q = P; q < 32; q *= 2) t += __shfl_xor_sync(0xffffffffu, t, q);
+    for (int i = 0; i < 16; i += 4)
+        if (i + lane / 8 < nw) t += red[i * 8 + lane];
+    t += __shfl_xor_sync(0xffffffffu, t, 8);
+    t += __shfl_xor_sync(0xffffffffu, t, 16);
 #pragma unroll
     for (int j = 0; j < NR; ++j) v[j] = __shfl_sync(0xffffffffu, t, j);
 }
 
+// An array's columns c, c + 1, .. of a piece (NULL: 1); what lies behind the row's end is 0.
+template <int V>
+__device__ __forceinline__ void load_columns(const float* g, int c, int H, float2 (&v)[V / 2]) {
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) v[j] = both(c < H && !g ? 1.0f : 0.0f);
+    if constexpr (V == 8) {
+        if (c >= H || !g) return;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(g + c) + j);
+            v[2 * j] = make_float2(f.x, f.y);
+            v[2 * j + 1] = make_float2(f.z, f.w);
+        }
+    } else {
+        if (g && c < H) v[0].x = __ldg(g + c);
+        if (g && c + 1 < H) v[0].y = __ldg(g + c + 1);
+        if (c + 1 >= H) v[0].y = 0.0f;
+    }
+}
 // The branch's factor of each column: y_scale * gate * post_gain.
 template <int V>
-__device__ __forceinline__ void load_branch(const NormArgs& a, int c, float (&b)[V]) {
-    float p[V];
-    load_gain<V>(a.gate, c, b);
-    load_gain<V>(a.post, c, p);
+__device__ __forceinline__ void load_branch(const NormArgs& a, int c, float2 (&b)[V / 2]) {
+    float2 p[V / 2];
+    load_columns<V>(a.gate, c, a.H, b);
+    load_columns<V>(a.post, c, a.H, p);
 #pragma unroll
-    for (int j = 0; j < V; ++j) b[j] *= a.ys * p[j];
+    for (int j = 0; j < V / 2; ++j) b[j] = __fmul2_rn(b[j], __fmul2_rn(both(a.ys), p[j]));
 }
 
+// Sum of squares of a thread's pieces, in fp64 (rows beyond fp32's range).
+template <typename T, int V, int N>
+__device__ __forceinline__ double squares64(const Piece<T, V> (&r)[N]) {
+    double d = 0.0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float2 v[V / 2];
+        r[i].get(v);
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) d += (double)v[j].x * v[j].x + (double)v[j].y * v[j].y;
+    }
+    return d;
+}
+// 1 / rms of a row held by the block.
+template <typename T, int V, int N>
+__device__ __forceinline__ float row_scale(const Piece<T, V> (&r)[N], int H, float inv, float eps, float* red, double* red64) {
+    float2 acc = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float2 v[V / 2];
+        r[i].get(v);
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) acc = __ffma2_rn(v[j], v[j], acc);
+    }
+    float ss[1] = {acc.x + acc.y};
+    block_sums(ss, red);
+    if (sum_ok(ss[0], eps)) return rsqrtf(fmaf(ss[0], inv, eps));
+    double dd[1] = {squares64<T, V, N>(r)};
+    block_sum<double, 1>(dd, red64);
+    return rms_scale(dd[0], H, eps);
+}
+
+// At 2048 x 6144 bf16 (x, y, x_out, n: 101 MB) the launch bound of 80 registers
+// lets two blocks of 384 threads share an SM, one row's sums under another's copies.
 template <typename XT, typename YT, typename NT, int V, int N>
-__global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
-    __shared__ float red[2][32 * 8];
+__global__ void __launch_bounds__(768) block_norm_kernel(const NormArgs a) {
+    __shared__ float red[2][16 * 8];
     __shared__ double red64[2][32];
     extern __shared__ __align__(16) unsigned char ring_mem[];
-    const int H = a.H, stages = a.stages;
-    const uint32_t ring = smem_addr(ring_mem);
-    const uint32_t xb = V == 8 ? ring_bytes<XT, N>() : 0, yb = V == 8 && a.has_prev ? ring_bytes<YT, N>() : 0;
-    const XT* x = (const XT*)a.x;
-    const YT* y = (const YT*)a.y;
-    auto prefetch = [&](int t, int slot) {
+    const int H = a.H, stages = a.stages, c0 = threadIdx.x * V;
+    const bool has_prev = a.has_prev, post = a.post_norm, has_next = a.has_next;
+    const float inv = 1.0f / (float)H;
+    const uint32_t xb = V == 8 ? ring_bytes<XT, N>() : 0;
+    const uint32_t slot_bytes = V == 8 ? xb + ring_bytes<YT, N>() : 0;
+    const uint32_t ring = smem_addr(ring_mem) + threadIdx.x * 16;
+    if constexpr (V == 8)
+        for (int i = 0; i < stages; ++i) {
+            ring_clear<XT, N>(ring + i * slot_bytes, false, H);
+            ring_clear<YT, N>(ring + i * slot_bytes + xb, !has_prev, H);
+        }
+    const XT* px = (const XT*)a.x + (size_t)blockIdx.x * a.ldx + c0;  // this thread's first column of the next row to copy
+    const YT* py = (const YT*)a.y + (size_t)blockIdx.x * a.ldy + c0;
+    int pt = blockIdx.x;
+    auto prefetch = [&](int slot) {
         if constexpr (V == 8) {
-            if (t < a.T) {
-                ring_copy<XT, N>(ring + slot * (xb + yb), x + (size_t)t * a.ldx, H);
-                if (a.has_prev) ring_copy<YT, N>(ring + slot * (xb + yb) + xb, y + (size_t)t * a.ldy, H);
+            if (pt < a.T) {
+                ring_copy<XT, N>(ring + slot * slot_bytes, px, H);
+                if (has_prev) ring_copy<YT, N>(ring + slot * slot_bytes + xb, py, H);
             }
             cp_async_commit();
+            pt += gridDim.x;
+            px += a.ldx * gridDim.x;
+            py += a.ldy * gridDim.x;
         }
     };
-    for (int i = 0; i < stages - 1; ++i) prefetch(blockIdx.x + i * gridDim.x, i);
-    if (stages == 1) prefetch(blockIdx.x, 0);
-    float b[N * V], q[N * V];
+    for (int i = 0; i < (stages > 1 ? stages - 1 : 1); ++i) prefetch(i);
+    float2 b[N * V / 2], q[N * V / 2];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * V;
-        float f[V];
+        float2 f[V / 2];
+        if (has_prev) load_branch<V>(a, c, f);
 #pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = 0.0f;
-        if (a.has_prev && c < H) load_branch<V>(a, c, f);
+        for (int j = 0; j < V / 2; ++j) b[i * V / 2 + j] = f[j];
+        if (has_next) load_columns<V>(a.pre, c, H, f);
 #pragma unroll
-        for (int j = 0; j < V; ++j) b[i * V + j] = f[j];
-        if (a.has_next && c < H) load_gain<V>(a.pre, c, f);
-#pragma unroll
-        for (int j = 0; j < V; ++j) q[i * V + j] = f[j];
+        for (int j = 0; j < V / 2; ++j) q[i * V / 2 + j] = f[j];
     }
     int slot = 0;
     for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-        Raw<XT, V> rx[N];
-        Raw<YT, V> ry[N];
+        Piece<XT, V> rx[N];
+        Piece<YT, V> ry[N];
         if constexpr (V == 8) {
             cp_async_wait(stages);
             // into the slot of the row before this one, which this thread has read
-            if (stages > 1) prefetch(t + (stages - 1) * gridDim.x, slot == 0 ? stages - 1 : slot - 1);
+            if (stages > 1) prefetch(slot == 0 ? stages - 1 : slot - 1);
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            take<XT, V>(rx[i], true, i, ring + slot * (xb + yb), x + (size_t)t * a.ldx, H);
-            take<YT, V>(ry[i], a.has_prev, i, ring + slot * (xb + yb) + xb, y + (size_t)t * a.ldy, H);
+            take<XT, V>(rx[i], true, i, ring + slot * slot_bytes, (const XT*)a.x + (size_t)t * a.ldx + c0, H);
+            take<YT, V>(ry[i], has_prev, i, ring + slot * slot_bytes + xb, (const YT*)a.y + (size_t)t * a.ldy + c0, H);
         }
-        if (stages == 1) prefetch(t + gridDim.x, 0);
+        if (stages == 1) prefetch(0);
         slot = slot + 1 >= stages ? 0 : slot + 1;
-        float ss[1] = {0.0f};
-        if (a.has_prev) {
-            float scale = a.token ? a.token[t] : 1.0f;
-            if (a.post_norm) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    float v[V];
-                    ry[i].get(v);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) ss[0] = fmaf(v[j], v[j], ss[0]);
-                }
-                block_sums<1>(ss, red[0]);
-                float rho = rms_scale(ss[0], H, a.eps_post);
-                if (!sum_ok(ss[0], a.eps_post)) {
-                    double dd[1] = {0.0};
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        float v[V];
-                        ry[i].get(v);
-#pragma unroll
-                        for (int j = 0; j < V; ++j) dd[0] += (double)v[j] * v[j];
-                    }
-                    block_sum<double, 1>(dd, red64[0]);
-                    rho = rms_scale(dd[0], H, a.eps_post);
-                }
-#pragma unroll
-                for (int i = 0; i < N; ++i) {  // y rho first: a row of large values times a small gate stays finite
-                    float vx[V], vy[V];
-                    rx[i].get(vx);
-                    ry[i].get(vy);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) vx[j] = fmaf(scale * b[i * V + j], vy[j] * rho, a.xs * vx[j]);
-                    rx[i].set(vx);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    float vx[V], vy[V];
-                    rx[i].get(vx);
-                    ry[i].get(vy);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) vx[j] = fmaf(scale * b[i * V + j], vy[j], a.xs * vx[j]);
-                    rx[i].set(vx);
-                }
-            }
+        if (has_prev) {
+            float w = a.token ? a.token[t] : 1.0f;
+            if (post) w *= row_scale<YT, V, N>(ry, H, inv, a.eps_post, red[0], red64[0]);
+            XT* xo = (XT*)a.xo + (size_t)t * a.ldxo + c0;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int c = (i * blockDim.x + threadIdx.x) * V;
-                if (c < H) rx[i].store((XT*)a.xo + (size_t)t * a.ldxo + c);
-                else rx[i].zero();
+                float2 x[V / 2], y[V / 2];
+                rx[i].get(x);
+                ry[i].get(y);
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j)
+                    x[j] = __ffma2_rn(b[i * V / 2 + j], __fmul2_rn(both(w), y[j]), __fmul2_rn(both(a.xs), x[j]));
+                rx[i].set(x);  // from here on as stored: what a later read of x_out sees
+                const int left = H - (int)(i * blockDim.x + threadIdx.x) * V;
+                if (left > 0) rx[i].store(xo + i * blockDim.x * V, left);
+                if (left < V) {
+                    if (left <= 0) rx[i].zero();
+                    else if constexpr (V == 2) rx[i].b.zero();
+                }
             }
         }
-        if (!a.has_next) {
-            if (a.post_norm) __syncthreads();  // the next row's sum reuses red[0]
-            continue;
-        }
-        ss[0] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float v[V];
-            rx[i].get(v);  // as stored: what a later read of x_out sees
-#pragma unroll
-            for (int j = 0; j < V; ++j) ss[0] = fmaf(v[j], v[j], ss[0]);
-        }
-        block_sums<1>(ss, red[1]);
-        float r = rms_scale(ss[0], H, a.eps_pre);
-        if (!sum_ok(ss[0], a.eps_pre)) {
-            double dd[1] = {0.0};
+        if (has_next) {
+            const float2 r = both(row_scale<XT, V, N>(rx, H, inv, a.eps_pre, red[1], red64[1]));
+            NT* no = (NT*)a.n + (size_t)t * a.ldn + c0;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                float v[V];
+                float2 v[V / 2];
                 rx[i].get(v);
 #pragma unroll
-                for (int j = 0; j < V; ++j) dd[0] += (double)v[j] * v[j];
+                for (int j = 0; j < V / 2; ++j) v[j] = __fmul2_rn(__fmul2_rn(v[j], r), q[i * V / 2 + j]);
+                const int left = H - (int)(i * blockDim.x + threadIdx.x) * V;
+                Piece<NT, V> out;
+                out.set(v);
+                if (left > 0) out.store(no + i * blockDim.x * V, left);
             }
-            block_sum<double, 1>(dd, red64[1]);
-            r = rms_scale(dd[0], H, a.eps_pre);
         }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * V;
-            if (c >= H) continue;
-            float v[V];
-            rx[i].get(v);
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = v[j] * r * q[i * V + j];
-            Raw<NT, V> out;
-            out.set(v);
-            out.store((NT*)a.n + (size_t)t * a.ldn + c);
-        }
-        if (!a.has_prev || !a.post_norm) __syncthreads();  // the next row's sum reuses red[1]
+        // with one sum a row, the next row's would use the same buffer
+        if (!(has_prev && post && has_next)) __syncthreads();
     }
 }
 
@@ -397,71 +501,77 @@ __global__ void __launch_bounds__(1024) block_norm_wide_kernel(NormArgs a) {
 // ---------------------------------------------------------------------------
 template <typename XT, typename YT, typename NT, int V, int N>
 __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs a) {
-    __shared__ float red[2][32 * 8];
+    __shared__ float red[2][16 * 8];
     __shared__ double red64[32 * 6];
     extern __shared__ __align__(16) unsigned char ring_mem[];
-    const int H = a.H, stages = a.stages;
-    const uint32_t ring = smem_addr(ring_mem);
-    const bool has_o = a.dxo != nullptr;
+    const int H = a.H, stages = a.stages, c0 = threadIdx.x * V;
+    const bool has_prev = a.has_prev, has_next = a.has_next, has_o = a.dxo != nullptr, post = a.post_norm;
     uint32_t yo = 0, oo = 0, no = 0, slot_bytes = 0;  // offsets of y, dxo and dn in a slot
     if constexpr (V == 8) {
         yo = ring_bytes<XT, N>();
-        oo = yo + (a.has_prev ? ring_bytes<YT, N>() : 0);
-        no = oo + (has_o ? ring_bytes<XT, N>() : 0);
-        slot_bytes = no + (a.has_next ? ring_bytes<NT, N>() : 0);
+        oo = yo + ring_bytes<YT, N>();
+        no = oo + ring_bytes<XT, N>();
+        slot_bytes = no + ring_bytes<NT, N>();
     }
-    const XT *s_ = (const XT*)a.x, *o_ = (const XT*)a.dxo;
-    const YT* y_ = (const YT*)a.y;
-    const NT* n_ = (const NT*)a.dn;
-    auto prefetch = [&](int t, int slot) {
+    const uint32_t ring = smem_addr(ring_mem) + threadIdx.x * 16;
+    if constexpr (V == 8)
+        for (int i = 0; i < stages; ++i) {
+            ring_clear<XT, N>(ring + i * slot_bytes, false, H);
+            ring_clear<YT, N>(ring + i * slot_bytes + yo, !has_prev, H);
+            ring_clear<XT, N>(ring + i * slot_bytes + oo, !has_o, H);
+            ring_clear<NT, N>(ring + i * slot_bytes + no, !has_next, H);
+        }
+    int pt = blockIdx.x;  // the next row to copy
+    auto prefetch = [&](int slot) {
         if constexpr (V == 8) {
-            if (t < a.T) {
+            if (pt < a.T) {
                 const uint32_t at = ring + slot * slot_bytes;
-                ring_copy<XT, N>(at, s_ + (size_t)t * a.ldx, H);
-                if (a.has_prev) ring_copy<YT, N>(at + yo, y_ + (size_t)t * a.ldy, H);
-                if (has_o) ring_copy<XT, N>(at + oo, o_ + (size_t)t * a.lddxo, H);
-                if (a.has_next) ring_copy<NT, N>(at + no, n_ + (size_t)t * a.lddn, H);
+                ring_copy<XT, N>(at, (const XT*)a.x + (size_t)pt * a.ldx + c0, H);
+                if (has_prev) ring_copy<YT, N>(at + yo, (const YT*)a.y + (size_t)pt * a.ldy + c0, H);
+                if (has_o) ring_copy<XT, N>(at + oo, (const XT*)a.dxo + (size_t)pt * a.lddxo + c0, H);
+                if (has_next) ring_copy<NT, N>(at + no, (const NT*)a.dn + (size_t)pt * a.lddn + c0, H);
             }
             cp_async_commit();
+            pt += gridDim.x;
         }
     };
-    for (int i = 0; i < stages - 1; ++i) prefetch(blockIdx.x + i * gridDim.x, i);
-    if (stages == 1) prefetch(blockIdx.x, 0);
-    float b[N * V], q[N * V], dq[N * V], A[N * V];
+    for (int i = 0; i < (stages > 1 ? stages - 1 : 1); ++i) prefetch(i);
+    constexpr int P = V / 2;
+    float2 b[N * P], q[N * P], dq[N * P], A[N * P];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * V;
-        float f[V];
+        float2 f[P], g[P];
 #pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = 0.0f;
-        if (a.has_prev && c < H) load_branch<V>(a, c, f);
+        for (int j = 0; j < P; ++j) f[j] = g[j] = both(0.0f);
+        if (has_prev) load_branch<V>(a, c, f);
+        if (has_next) load_columns<V>(a.pre, c, H, g);
 #pragma unroll
-        for (int j = 0; j < V; ++j) b[i * V + j] = f[j];
-        if (a.has_next && c < H) load_gain<V>(a.pre, c, f);
-#pragma unroll
-        for (int j = 0; j < V; ++j) q[i * V + j] = f[j], dq[i * V + j] = A[i * V + j] = 0.0f;
+        for (int j = 0; j < P; ++j) b[i * P + j] = f[j], q[i * P + j] = g[j], dq[i * P + j] = A[i * P + j] = both(0.0f);
     }
     int slot = 0, flip = 0;
     const float inv = 1.0f / (float)H;
+    const bool tiny_s = has_next && a.eps_pre < 1e-12f, tiny_y = post && a.eps_post < 1e-12f;  // see sum_ok
     for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
         if constexpr (V == 8) {
             cp_async_wait(stages);
-            if (stages > 1) prefetch(t + (stages - 1) * gridDim.x, slot == 0 ? stages - 1 : slot - 1);
+            // into the slot of the row before this one, which this thread has read
+            if (stages > 1) prefetch(slot == 0 ? stages - 1 : slot - 1);
         }
         const uint32_t at = ring + slot * slot_bytes;
         slot = slot + 1 >= stages ? 0 : slot + 1;
         // Wide pieces are read from the ring in every pass over the row; single columns stay in registers.
         constexpr int kKept = V == 8 ? 1 : N;
-        Raw<XT, V> rs[kKept], ro[kKept];
-        Raw<YT, V> ry[kKept];
-        Raw<NT, V> rn[kKept];
-        auto row = [&](int i, int pass, float (&s)[V], float (&y)[V], float (&o)[V], float (&n)[V]) {
+        Piece<XT, V> rs[kKept], ro[kKept];
+        Piece<YT, V> ry[kKept];
+        Piece<NT, V> rn[kKept];
+        auto row = [&](int i, int pass, float2 (&s)[P], float2 (&y)[P], float2 (&o)[P], float2 (&n)[P]) {
             const int k = V == 8 ? 0 : i;
             if (V == 8 || pass == 0) {
-                take<XT, V>(rs[k], true, i, at, s_ + (size_t)t * a.ldx, H);
-                take<YT, V>(ry[k], a.has_prev, i, at + yo, y_ + (size_t)t * a.ldy, H);
-                take<XT, V>(ro[k], has_o, i, at + oo, o_ + (size_t)t * a.lddxo, H);
-                take<NT, V>(rn[k], a.has_next, i, at + no, n_ + (size_t)t * a.lddn, H);
+                take<XT, V>(rs[k], true, i, at, (const XT*)a.x + (size_t)t * a.ldx + c0, H);
+                take<YT, V>(ry[k], has_prev, i, at + yo, (const YT*)a.y + (size_t)t * a.ldy + c0, H);
+                take<XT, V>(ro[k], has_o, i, at + oo, (const XT*)a.dxo + (size_t)t * a.lddxo + c0, H);
+                take<NT, V>(rn[k], has_next, i, at + no, (const NT*)a.dn + (size_t)t * a.lddn + c0, H);
             }
             rs[k].get(s);
             ry[k].get(y);
@@ -469,106 +579,117 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
             rn[k].get(n);
         };
         const float u = a.token ? a.token[t] : 1.0f;
-        float v[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        float2 acc[6];
+#pragma unroll
+        for (int j = 0; j < 6; ++j) acc[j] = both(0.0f);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            float s[V], n[V], y[V], o[V];
+            float2 s[P], n[P], y[P], o[P];
             row(i, 0, s, y, o, n);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float qn = q[i * V + j] * n[j], by = b[i * V + j] * y[j];
-                v[0] = fmaf(s[j], s[j], v[0]);
-                v[1] = fmaf(s[j], qn, v[1]);
-                v[2] = fmaf(y[j], y[j], v[2]);
-                v[3] = fmaf(by, o[j], v[3]);
-                v[4] = fmaf(by, qn, v[4]);
-                v[5] = fmaf(by, s[j], v[5]);
+            for (int j = 0; j < P; ++j) {
+                const float2 qn = __fmul2_rn(q[i * P + j], n[j]), by = __fmul2_rn(b[i * P + j], y[j]);
+                acc[0] = __ffma2_rn(s[j], s[j], acc[0]);
+                acc[1] = __ffma2_rn(s[j], qn, acc[1]);
+                acc[2] = __ffma2_rn(y[j], y[j], acc[2]);
+                acc[3] = __ffma2_rn(by, o[j], acc[3]);
+                acc[4] = __ffma2_rn(by, qn, acc[4]);
+                acc[5] = __ffma2_rn(by, s[j], acc[5]);
             }
         }
-        block_sums<6>(v, red[flip]);
+        float v[6];
+#pragma unroll
+        for (int j = 0; j < 6; ++j) v[j] = acc[j].x + acc[j].y;
+        block_sums(v, red[flip]);
         flip ^= 1;
         float r = 0.0f, m1 = 0.0f, rho = 1.0f, du;
-        bool ok = (!a.has_next || sum_ok(v[0], a.eps_pre)) && (!a.post_norm || sum_ok(v[2], a.eps_post));
-#pragma unroll
-        for (int j = 0; j < 6; ++j) ok = ok && fabsf(v[j]) <= 3e37f;
-        if (ok) {
-            if (a.has_next) {
-                r = rms_scale(v[0], H, a.eps_pre);
+        // every sum finite and in range (not so with NaN), no squares lost that eps does not hide
+        const float big = fabsf(v[0]) + fabsf(v[1]) + fabsf(v[2]) + fabsf(v[3]) + fabsf(v[4]) + fabsf(v[5]);
+        if (big <= 3e37f && !(tiny_s && v[0] < 1e-24f) && !(tiny_y && v[2] < 1e-24f)) {
+            if (has_next) {
+                r = rsqrtf(fmaf(v[0], inv, a.eps_pre));
                 m1 = v[1] * r * inv;
             }
-            if (a.post_norm) rho = rms_scale(v[2], H, a.eps_post);
+            if (post) rho = rsqrtf(fmaf(v[2], inv, a.eps_post));
             du = rho * fmaf(r, fmaf(-r * m1, v[5], v[4]), v[3]);
         } else {  // a row beyond fp32's range (or not finite): the same sums in fp64
             double w[6] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                float s[V], n[V], y[V], o[V];
-                row(i, 1, s, y, o, n);
+                float2 s2[P], n2[P], y2[P], o2[P];
+                row(i, 1, s2, y2, o2, n2);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const double qn = (double)q[i * V + j] * n[j], by = (double)b[i * V + j] * y[j];
-                    w[0] += (double)s[j] * s[j];
-                    w[1] += s[j] * qn;
-                    w[2] += (double)y[j] * y[j];
-                    w[3] += by * o[j];
+                    const int k = j / 2;
+                    const bool hi = j & 1;
+                    const double s = hi ? s2[k].y : s2[k].x, y = hi ? y2[k].y : y2[k].x, o = hi ? o2[k].y : o2[k].x;
+                    const double qn = (double)(hi ? q[i * P + k].y : q[i * P + k].x) * (hi ? n2[k].y : n2[k].x);
+                    const double by = (double)(hi ? b[i * P + k].y : b[i * P + k].x) * y;
+                    w[0] += s * s;
+                    w[1] += s * qn;
+                    w[2] += y * y;
+                    w[3] += by * o;
                     w[4] += by * qn;
-                    w[5] += by * s[j];
+                    w[5] += by * s;
                 }
             }
             block_sum<double, 6>(w, red64);
             __syncthreads();  // the next such row reuses red64
             double rd = 0.0, md = 0.0, pd = 1.0;
-            if (a.has_next) {
+            if (has_next) {
                 rd = 1.0 / sqrt(w[0] / H + (double)a.eps_pre);
                 md = w[1] * rd / H;
             }
-            if (a.post_norm) pd = 1.0 / sqrt(w[2] / H + (double)a.eps_post);
+            if (post) pd = 1.0 / sqrt(w[2] / H + (double)a.eps_post);
             r = (float)rd;
             m1 = (float)md;
             rho = (float)pd;
             du = (float)(pd * (w[3] + rd * (w[4] - rd * md * w[5])));
         }
         if (a.dtoken && threadIdx.x == 0) a.dtoken[t] = du;
-        const float m2 = a.post_norm ? u * du * inv : 0.0f;
+        const float2 m2 = both(post ? -u * du * inv : 0.0f), r2 = both(r), m1n = both(-m1), rho2 = both(rho), u2 = both(u);
+        XT* dx = (XT*)a.dx + (size_t)t * a.lddx + c0;
+        YT* dy = (YT*)a.dy + (size_t)t * a.lddy + c0;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * V;
-            float s[V], n[V], y[V], o[V];
+            float2 s[P], n[P], y[P], o[P];
             row(i, 1, s, y, o, n);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int k = i * V + j;
-                const float sh = s[j] * r, yh = y[j] * rho;
-                dq[k] = fmaf(sh, n[j], dq[k]);
-                o[j] = fmaf(r, fmaf(-sh, m1, q[k] * n[j]), o[j]);
-                A[k] = fmaf(u * yh, o[j], A[k]);
-                y[j] = rho * fmaf(-yh, m2, u * b[k] * o[j]);
-                o[j] *= a.xs;
+            for (int j = 0; j < P; ++j) {
+                const int k = i * P + j;
+                const float2 sh = __fmul2_rn(s[j], r2), yh = __fmul2_rn(y[j], rho2);
+                dq[k] = __ffma2_rn(sh, n[j], dq[k]);
+                o[j] = __ffma2_rn(r2, __ffma2_rn(sh, m1n, __fmul2_rn(q[k], n[j])), o[j]);  // ds
+                const float2 uo = __fmul2_rn(u2, o[j]);
+                A[k] = __ffma2_rn(yh, uo, A[k]);
+                y[j] = __fmul2_rn(rho2, __ffma2_rn(yh, m2, __fmul2_rn(b[k], uo)));
+                o[j] = __fmul2_rn(both(a.xs), o[j]);
             }
-            if (c >= H) continue;
+            const int left = H - (int)(i * blockDim.x + threadIdx.x) * V;
+            if (left <= 0) continue;
             if (a.dx) {
-                Raw<XT, V> out;
+                Piece<XT, V> out;
                 out.set(o);
-                out.store((XT*)a.dx + (size_t)t * a.lddx + c);
+                out.store(dx + i * blockDim.x * V, left);
             }
             if (a.dy) {
-                Raw<YT, V> out;
+                Piece<YT, V> out;
                 out.set(y);
-                out.store((YT*)a.dy + (size_t)t * a.lddy + c);
+                out.store(dy + i * blockDim.x * V, left);
             }
         }
-        if (stages == 1) prefetch(t + gridDim.x, 0);
+        if (stages == 1) prefetch(0);
     }
     if (a.part) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * V;
-            if (c >= H) continue;
             float* out = a.part + (size_t)blockIdx.x * 2 * H + c;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                out[j] = dq[i * V + j];
-                out[(size_t)H + j] = A[i * V + j];
+                if (c + j >= H) break;
+                out[j] = j & 1 ? dq[i * P + j / 2].y : dq[i * P + j / 2].x;
+                out[(size_t)H + j] = j & 1 ? A[i * P + j / 2].y : A[i * P + j / 2].x;
             }
         }
     }
@@ -627,10 +748,14 @@ __global__ void __launch_bounds__(1024) block_norm_backward_wide_kernel(NormArgs
         float m2 = 0.0f;
         for (int round = 0; round < 2; ++round) {
             for (int c = threadIdx.x; c < H; c += blockDim.x) {
-                float s, y, n, o, q[1], b[1] = {0.0f};
+                float s, y, n, o, q[1], b[1] = {0.0f}, p[1];
                 row(c, s, y, n, o);
                 load_gain<1>(a.pre, c, q);
-                if (a.has_prev) load_branch<1>(a, c, b);
+                if (a.has_prev) {
+                    load_gain<1>(a.gate, c, b);
+                    load_gain<1>(a.post, c, p);
+                    b[0] *= a.ys * p[0];
+                }
                 const float sh = s * r;
                 if (a.has_next) o = fmaf(r, fmaf(-sh, m1, q[0] * n), o);
                 const float yh = y * rho;
@@ -696,7 +821,7 @@ struct Shape {
     int V, N, threads;
 };
 Shape shape_of(int H, bool vec) {
-    const int V = vec ? 8 : 1;
+    const int V = vec ? 8 : 2;
     const int n = (H + V - 1) / V;
     for (int N : {1, 2, 4, 8}) {
         if (vec && N > 2) break;
@@ -707,25 +832,30 @@ Shape shape_of(int H, bool vec) {
 }
 
 constexpr int kSms = 148;
-// Blocks of `threads` that share an SM, and so the grid of a persistent launch.
-int blocks_per_sm(int threads) { return threads >= 512 ? 1 : threads >= 256 ? 2 : threads >= 128 ? 4 : 8; }
-int grid_of(int T, int H) {  // the same for aligned and unaligned rows: the workspace's size depends on it
-    const int vec_threads = shape_of(H, true).threads, threads = H % 8 ? shape_of(H, false).threads : vec_threads;
-    const int g = kSms * blocks_per_sm(threads < vec_threads ? threads : vec_threads);
+// Blocks that share an SM: as many as their registers let (80 a thread
+// forward, 128 backward), at most 8.
+int blocks_per_sm(int threads, bool fwd) {
+    const int n = (fwd ? 768 : 512) / threads;
+    return n < 1 ? 1 : n > 8 ? 8 : n;
+}
+// Blocks of a persistent launch over T rows. The workspace's size depends on
+// it: it must not depend on the alignment of a call's rows.
+int grid_of(int T, int H, bool fwd) {
+    const int g = kSms * blocks_per_sm(shape_of(H, H % 8 == 0).threads, fwd);
     return T < g ? T : g;
 }
 // Ring slots of `row` bytes (at most 128 KB) that fit beside the other blocks of an SM.
-int stages_of(size_t row, int threads, int rows) {
-    const size_t n = 200 * 1024 / blocks_per_sm(threads) / row;
+int stages_of(size_t row, int threads, int rows, bool fwd) {
+    const size_t n = 200 * 1024 / blocks_per_sm(threads, fwd) / row;
     return n < 1 || rows < 2 ? 1 : n > 4 ? 4 : (int)n;
 }
 
 using B = __nv_bfloat16;
 using Kernel = void (*)(NormArgs);
 
-cudaError_t launch_rows(Kernel k, NormArgs& a, const Shape& s, size_t col_bytes, int grid, cudaStream_t st) {
+cudaError_t launch_rows(Kernel k, NormArgs& a, const Shape& s, size_t col_bytes, int grid, bool fwd, cudaStream_t st) {
     const size_t row = s.V == 8 && s.N ? col_bytes * 8 * s.N * s.threads : 0;
-    a.stages = row ? stages_of(row, s.threads, (a.T + grid - 1) / grid) : 0;
+    a.stages = row ? stages_of(row, s.threads, (a.T + grid - 1) / grid, fwd) : 0;
     const size_t smem = a.stages * row;
     if (smem > 40 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -739,11 +869,11 @@ cudaError_t forward_typed(NormArgs& a, bool vec, cudaStream_t st) {
     const Shape s = shape_of(a.H, vec);
     const Kernel k = s.N == 0   ? block_norm_wide_kernel<XT, YT, NT>
                      : s.V == 8 ? (s.N == 1 ? block_norm_kernel<XT, YT, NT, 8, 1> : block_norm_kernel<XT, YT, NT, 8, 2>)
-                     : s.N == 1 ? block_norm_kernel<XT, YT, NT, 1, 1>
-                     : s.N == 2 ? block_norm_kernel<XT, YT, NT, 1, 2>
-                     : s.N == 4 ? block_norm_kernel<XT, YT, NT, 1, 4>
-                                : block_norm_kernel<XT, YT, NT, 1, 8>;
-    return launch_rows(k, a, s, sizeof(XT) + (a.has_prev ? sizeof(YT) : 0), s.N ? grid_of(a.T, a.H) : a.T, st);
+                     : s.N == 1 ? block_norm_kernel<XT, YT, NT, 2, 1>
+                     : s.N == 2 ? block_norm_kernel<XT, YT, NT, 2, 2>
+                     : s.N == 4 ? block_norm_kernel<XT, YT, NT, 2, 4>
+                                : block_norm_kernel<XT, YT, NT, 2, 8>;
+    return launch_rows(k, a, s, sizeof(XT) + sizeof(YT), s.N ? grid_of(a.T, a.H, true) : a.T, true, st);
 }
 
 template <typename XT, typename YT, typename NT>
@@ -752,12 +882,12 @@ cudaError_t backward_typed(NormArgs& a, bool vec, cudaStream_t st) {
     const Kernel k = s.N == 0 ? block_norm_backward_wide_kernel<XT, YT, NT>
                      : s.V == 8
                          ? (s.N == 1 ? block_norm_backward_kernel<XT, YT, NT, 8, 1> : block_norm_backward_kernel<XT, YT, NT, 8, 2>)
-                     : s.N == 1 ? block_norm_backward_kernel<XT, YT, NT, 1, 1>
-                     : s.N == 2 ? block_norm_backward_kernel<XT, YT, NT, 1, 2>
-                     : s.N == 4 ? block_norm_backward_kernel<XT, YT, NT, 1, 4>
-                                : block_norm_backward_kernel<XT, YT, NT, 1, 8>;
-    const size_t col = sizeof(XT) * (a.dxo ? 2 : 1) + (a.has_prev ? sizeof(YT) : 0) + (a.has_next ? sizeof(NT) : 0);
-    return launch_rows(k, a, s, col, grid_of(a.T, a.H), st);
+                     : s.N == 1 ? block_norm_backward_kernel<XT, YT, NT, 2, 1>
+                     : s.N == 2 ? block_norm_backward_kernel<XT, YT, NT, 2, 2>
+                     : s.N == 4 ? block_norm_backward_kernel<XT, YT, NT, 2, 4>
+                                : block_norm_backward_kernel<XT, YT, NT, 2, 8>;
+    const size_t col = 2 * sizeof(XT) + sizeof(YT) + sizeof(NT);
+    return launch_rows(k, a, s, col, grid_of(a.T, a.H, false), false, st);
 }
 
 template <bool fwd>
@@ -913,7 +1043,7 @@ COLI_API coli_status coli_block_norm(const coli_block_params* prev, const coli_b
 
 COLI_API int64_t coli_block_norm_workspace(int T, int H) {
     if (T < 0 || T > kBlockMaxTokens || H < 1 || H > kBlockMaxHidden) return -1;
-    return (int64_t)grid_of(T, H) * 2 * H * 4;
+    return (int64_t)grid_of(T, H, false) * 2 * H * 4;
 }
 
 COLI_API coli_status coli_block_norm_backward(const coli_block_params* prev, const coli_block_params* next,
@@ -998,6 +1128,6 @@ COLI_API coli_status coli_block_norm_backward(const coli_block_params* prev, con
         if (e != cudaSuccess) return block_cuda_fail(e, "block norm backward");
     }
     if (!want) return COLI_OK;
-    e = launch(sum_parts_kernel, dim3((H + 31) / 32, 2), 256, 0, s, T > 0, a, grid_of(T, H), dpre_gain, dpost_gain, dgate);
+    e = launch(sum_parts_kernel, dim3((H + 31) / 32, 2), 256, 0, s, T > 0, a, grid_of(T, H, false), dpre_gain, dpost_gain, dgate);
     return e == cudaSuccess ? COLI_OK : block_cuda_fail(e, "block norm backward: gains");
 }
