@@ -2,32 +2,80 @@
 // (coli_moe_route_backward).
 #include "block.cuh"
 
+#include <type_traits>
+
 #define COLI_API extern "C" __attribute__((visibility("default")))
 
 namespace coli {
 namespace {
 
 constexpr int kSms = 148;
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 
-// dlogits[t][k] = w_k (dw_k - sum_j w_j dw_j): the weights are a softmax over
-// the selected logits, whose Jacobian is diag(w) - w w^T. One warp a token.
-__global__ void __launch_bounds__(256) route_dlogits_kernel(const int32_t* ids, const float* w, const float* dw, int T,
-                                                            int K, int E, float* dl) {
-    const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (t < T) {
-        float wk = 0.0f, gk = 0.0f;
-        if (lane < K) {
-            const size_t i = (size_t)t * K + lane;
-            const int e = ids[i];
-            wk = (unsigned)e < (unsigned)E ? w[i] : 0.0f;
-            gk = wk != 0.0f ? dw[i] : 0.0f;  // an absent slot's dweights is not used
-        }
-        float m = wk * gk;
+// First index in [a, b) whose slot is >= bound (the list of an expert is
+// ascending): eight parts at a time, so four rounds of loads for 2048 slots.
+__device__ __forceinline__ int first_at_least(const int32_t* slot, int a, int b, int bound) {
+    while (b - a > 8) {
+        const int step = (b - a) >> 3;
+        int below = 0;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-        if (lane < K) dl[(size_t)t * K + lane] = wk != 0.0f ? wk * (gk - m) : 0.0f;
+        for (int j = 1; j < 8; ++j) below += slot[a + j * step - 1] < bound;
+        const int a0 = a;
+        a = a0 + below * step;
+        if (below < 7) b = a0 + (below + 1) * step;
+    }
+    int below = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) below += a + j < b && slot[a + j] < bound;
+    return a + below;
+}
+
+// What the sums need, once for all column slabs:
+//  - dlogits[t][k] = w_k (dw_k - sum_j w_j dw_j): the weights are a softmax over
+//    the selected logits, whose Jacobian is diag(w) - w w^T. One warp a token.
+//  - inv: the plan's row of each slot;
+//  - bound[c][e]: the first row of expert e whose token is >= c * chunk (of the
+//    last c: its end).
+// Blocks [0, n_tok) take tokens, [n_tok, n_tok + n_inv) rows, the others bounds.
+struct Prep {
+    const int32_t *ids, *offsets, *slot;
+    const float *w, *dw;
+    float* dl;
+    int32_t *inv, *bound;
+    int T, K, E, chunk, n_chunks, n_tok, n_inv;
+};
+__global__ void __launch_bounds__(256) route_prep_kernel(const Prep a) {
+    const int lane = threadIdx.x & 31, n = a.T * a.K;
+    if ((int)blockIdx.x < a.n_tok) {
+        const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
+        if (t < a.T) {
+            float wk = 0.0f, gk = 0.0f;
+            const size_t i = (size_t)t * a.K + lane;
+            if (lane < a.K) {
+                const int e = a.ids[i];
+                wk = (unsigned)e < (unsigned)a.E ? a.w[i] : 0.0f;
+                gk = wk != 0.0f ? a.dw[i] : 0.0f;  // an absent slot's dweights is not used
+            }
+            float m = wk * gk;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+            if (lane < a.K) a.dl[i] = wk != 0.0f ? wk * (gk - m) : 0.0f;
+        }
+    } else if ((int)blockIdx.x < a.n_tok + a.n_inv) {
+        const int q = (blockIdx.x - a.n_tok) * 256 + threadIdx.x;
+        if (q < n) {
+            const int i = a.slot[q];
+            if (i >= 0 && i < n) a.inv[i] = q;
+        }
+    } else {
+        const int j = (blockIdx.x - a.n_tok - a.n_inv) * 256 + threadIdx.x;
+        if (j < (a.n_chunks + 1) * a.E) {
+            const int c = j / a.E, e = j % a.E;
+            const int q0 = min(max(a.offsets[e], 0), n), q1 = min(max(a.offsets[e + 1], q0), n);
+            const int t = min(c * a.chunk, a.T);
+            a.bound[j] = t == 0 ? q0 : t == a.T ? q1 : first_at_least(a.slot, q0, q1, t * a.K);
+        }
     }
     grid_next();
 }
@@ -41,13 +89,46 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 // dx[t] = sum_k dlogits[t][k] Wr[ids[t][k]]. Every token reads K router rows:
 // at 2048 x 8 x 6144 that is 403 MB, against 6 MB of router. So a block keeps a
 // slab of 32 * VC columns of all E rows in shared memory and takes a share of
-// the tokens, one warp each, a lane VC columns: bound by shared memory reads
-// (13 us at those sizes). A slot that is absent reads a row of zeros.
+// the tokens; a warp takes four tokens at a time (K <= 8), a lane VC columns of each.
+// The slots' rows and factors go through a buffer of the warp's, from which
+// all lanes read two slots with one access. Bound by shared memory reads. A
+// slot that is absent reads a row of zeros.
 // ---------------------------------------------------------------------------
+struct SlotRef {
+    int row;  // its row's place in shared memory, in elements or bytes
+    float d;
+};
+
+template <int VC>
+struct Columns;
+template <>
+struct Columns<4> {
+    float4 v;
+    __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void add(float d, float2 (&acc)[2]) const {
+        acc[0] = __ffma2_rn(make_float2(d, d), make_float2(v.x, v.y), acc[0]);
+        acc[1] = __ffma2_rn(make_float2(d, d), make_float2(v.z, v.w), acc[1]);
+    }
+};
+template <>
+struct Columns<2> {
+    float2 v;
+    __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float2*>(p); }
+    __device__ __forceinline__ void add(float d, float2 (&acc)[1]) const { acc[0] = __ffma2_rn(make_float2(d, d), v, acc[0]); }
+};
+template <>
+struct Columns<1> {
+    float v;
+    __device__ __forceinline__ void load(const float* p) { v = *p; }
+    __device__ __forceinline__ void add(float d, float2 (&acc)[1]) const { acc[0].x = fmaf(d, v, acc[0].x); }
+};
+
 template <typename XT, int VC>
-__global__ void __launch_bounds__(kThreads) route_dx_kernel(const int32_t* ids, const float* dl, const float* wr, int T,
+// (one block an SM: without the second bound the compiler saves registers for four)
+__global__ void __launch_bounds__(kThreads, 1) route_dx_kernel(const int32_t* ids, const float* dl, const float* wr, int T,
                                                             int K, int E, int H, int per, bool vec, XT* dx, int64_t ldx) {
     extern __shared__ __align__(16) float slab[];  // [E + 1][32 * VC], the last row zero
+    __shared__ __align__(16) SlotRef refs[kWarps][2][32];
     constexpr int C = 32 * VC;
     const int c0 = blockIdx.x * C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (vec) {
@@ -63,75 +144,77 @@ __global__ void __launch_bounds__(kThreads) route_dx_kernel(const int32_t* ids, 
     }
     for (int i = threadIdx.x; i < C; i += kThreads) slab[E * C + i] = 0.0f;
     grid_wait();  // dlogits
+    // a warp's turn: its lanes hold the slots of G tokens, in groups of 8, 16 or 32 (zero rows behind the K-th)
+    const int sh = K <= 8 ? 3 : K <= 16 ? 4 : 5, G = 32 >> sh, tg = lane >> sh, tk = lane & ((1 << sh) - 1);
     const int t1 = min(T, (int)(blockIdx.y + 1) * per);
-    int t = blockIdx.y * per + warp;
-    auto fetch = [&](int at, int& e, float& d) {
-        e = E;
-        d = 0.0f;
-        if (at < t1 && lane < K) {
-            d = dl[(size_t)at * K + lane];
-            const int id = ids[(size_t)at * K + lane];
-            e = d != 0.0f && (unsigned)id < (unsigned)E ? id : E;
+    int t = blockIdx.y * per + warp * G;
+    auto fetch = [&](int at) {
+        SlotRef r{E * C, 0.0f};
+        if (tk < K && at + tg < t1) {
+            const int i = (at + tg) * K + tk;
+            const int id = ids[i];
+            r.d = dl[i];
+            if (r.d != 0.0f && (unsigned)id < (unsigned)E) r.row = id * C;
+            else r.d = 0.0f;
         }
+        return r;
     };
-    int e;
-    float d;
-    fetch(t, e, d);
+    SlotRef mine = fetch(t);
     cp_async_wait_all();
     __syncthreads();
-    const float* mine = slab + lane * VC;
+    const float* col = slab + lane * VC;
     const int left = H - c0 - lane * VC;
-    for (; t < t1; t += kWarps) {
-        int e1;
-        float d1;
-        fetch(t + kWarps, e1, d1);
-        float acc[VC];
+    for (int flip = 0; t < t1; t += kWarps * G, flip ^= 1) {
+        SlotRef* ref = refs[warp][flip];
+        ref[lane] = mine;
+        __syncwarp();
+        mine = fetch(t + kWarps * G);
+        for (int g = 0; g < G && t + g < t1; ++g) {
+            float2 sum[(VC + 1) / 2];
 #pragma unroll
-        for (int j = 0; j < VC; ++j) acc[j] = 0.0f;
-        for (int k0 = 0; k0 < K; k0 += 8) {
+            for (int j = 0; j < (VC + 1) / 2; ++j) sum[j] = make_float2(0.0f, 0.0f);
+            for (int k0 = 0; k0 < K; k0 += 8) {
+                int4 r[4];  // two slots each
+                Columns<VC> v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {  // lanes from K on hold the zero row
-                const int ek = __shfl_sync(0xffffffffu, e, k0 + k);
-                const float dk = __shfl_sync(0xffffffffu, d, k0 + k);
-                const float* row = mine + ek * C;
-                if constexpr (VC == 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(row);
-                    acc[0] = fmaf(dk, v.x, acc[0]);
-                    acc[1] = fmaf(dk, v.y, acc[1]);
-                    acc[2] = fmaf(dk, v.z, acc[2]);
-                    acc[3] = fmaf(dk, v.w, acc[3]);
-                } else if constexpr (VC == 2) {
-                    const float2 v = *reinterpret_cast<const float2*>(row);
-                    acc[0] = fmaf(dk, v.x, acc[0]);
-                    acc[1] = fmaf(dk, v.y, acc[1]);
-                } else {
-                    acc[0] = fmaf(dk, row[0], acc[0]);
+                for (int k = 0; k < 4; ++k) r[k] = reinterpret_cast<const int4*>(ref + (g << sh) + k0)[k];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[2 * k].load(col + r[k].x);
+                    v[2 * k + 1].load(col + r[k].z);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[2 * k].add(__int_as_float(r[k].y), sum);
+                    v[2 * k + 1].add(__int_as_float(r[k].w), sum);
                 }
             }
-        }
-        XT* out = dx + (size_t)t * ldx + c0 + lane * VC;
-        if (VC == 4 && vec) {
-            if (left > 0) {
-                if constexpr (sizeof(XT) == 4) {
-                    *reinterpret_cast<float4*>(out) = make_float4(acc[0], acc[1 % VC], acc[2 % VC], acc[3 % VC]);
-                } else {
-                    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[0], acc[1 % VC]), hi = __floats2bfloat162_rn(acc[2 % VC], acc[3 % VC]);
-                    *reinterpret_cast<uint2*>(out) =
-                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-                }
-            }
-        } else {
+            float acc[VC];
 #pragma unroll
-            for (int j = 0; j < VC; ++j)
-                if (j < left) {
-                    Raw<XT, 1> r;
-                    const float one[1] = {acc[j]};
-                    r.set(one);
-                    r.store(out + j);
+            for (int j = 0; j < VC; ++j) acc[j] = j & 1 ? sum[j / 2].y : sum[j / 2].x;
+            XT* out = dx + (size_t)(t + g) * ldx + c0 + lane * VC;
+            if (VC == 4 && vec) {
+                if (left > 0) {
+                    if constexpr (sizeof(XT) == 4) {
+                        *reinterpret_cast<float4*>(out) = make_float4(acc[0], acc[1 % VC], acc[2 % VC], acc[3 % VC]);
+                    } else {
+                        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[0], acc[1 % VC]),
+                                             hi = __floats2bfloat162_rn(acc[2 % VC], acc[3 % VC]);
+                        *reinterpret_cast<uint2*>(out) =
+                            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                    }
                 }
+            } else {
+#pragma unroll
+                for (int j = 0; j < VC; ++j)
+                    if (j < left) {
+                        Raw<XT, 1> one;
+                        const float f[1] = {acc[j]};
+                        one.set(f);
+                        one.store(out + j);
+                    }
+            }
         }
-        e = e1;
-        d = d1;
     }
     grid_next();
 }
@@ -139,63 +222,110 @@ __global__ void __launch_bounds__(kThreads) route_dx_kernel(const int32_t* ids, 
 // ---------------------------------------------------------------------------
 // drouter_w[e] and dbias[e]: sums over the expert's slots of dlogits * x[token].
 // Again a token's row is needed K times, so a block keeps 256 bytes of columns
-// of up to kChunk tokens in shared memory; a warp takes an expert and adds the
-// chunk's slots of that expert (found in its sorted list by bisection) in
-// order, two rows at a time, sixteen lanes each. A block's sums go to its
-// split's part of the workspace, which route_sum_kernel adds in order; with one
-// split they are the result. At 2048 x 8 x 6144 bf16: 25 MB of x once, bound by
-// the instructions that widen and add the 201 MB of rows.
+// of a chunk of tokens in shared memory, and beside them the chunk's slots in
+// expert order (their places follow from the plan). A warp takes an expert and
+// adds its rows in order, a lane 8 bytes of each. A block takes `per` chunks of
+// its split one after another; its sums go to the split's part of the
+// workspace, which route_sum_kernel adds in order; with one split they are the
+// result.
 // ---------------------------------------------------------------------------
 constexpr int kRowBytes = 256;
-constexpr int kChunk = 704;
+constexpr int kRoom = 224 * 1024;  // shared memory of a block
+constexpr int kFirst = 6;           // slots a thread asks for at once (all of a chunk's, with K <= 8)
 
-// First index in [a, b) whose slot is >= bound (the list of an expert is ascending).
-__device__ __forceinline__ int first_at_least(const int32_t* slot, int a, int b, int bound) {
-    while (a < b) {
-        const int m = (a + b) >> 1;
-        if (slot[m] < bound) a = m + 1;
-        else b = m;
+// Most tokens of a chunk: their rows, one zero row, their slots (an even number of each expert's), and two
+// numbers an expert fit.
+int chunk_of(int K, int E) { return (kRoom - kRowBytes - 16 * (E + 1)) / (kRowBytes + 8 * K); }
+
+// Exclusive prefix sums of v[0..n) in place (n <= 1024), the total behind them.
+__device__ __forceinline__ void prefix(int* v, int n, int* sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int i = 2 * threadIdx.x;
+    const int a = i < n ? v[i] : 0, b = i + 1 < n ? v[i + 1] : 0;
+    int s = a + b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += u;
     }
-    return a;
+    if (lane == 31) sums[warp] = s;
+    __syncthreads();
+    int before = s - a - b;
+    for (int w = 0; w < warp; ++w) before += sums[w];
+    if (i < n) v[i] = before;
+    if (i + 1 < n) v[i + 1] = before + a;
+    if (threadIdx.x == kThreads - 1) v[n] = before + a + b;
+    __syncthreads();
 }
 
+struct Rows {
+    const int32_t *ids, *inv, *bound;
+    const float* dl;
+    int T, K, E, H, chunk, n_chunks, per;
+    int64_t ldx;
+    int vec, vec_out;
+    float *part, *part_b;  // NULL: not wanted
+};
+
 template <typename XT>
-__global__ void __launch_bounds__(kThreads) route_rows_kernel(const int32_t* offsets, const int32_t* slot, const float* dl,
-                                                              int T, int K, int E, const XT* x, int64_t ldx, int H, int per,
-                                                              bool vec, bool vec_out, float* part, float* part_b) {
-    extern __shared__ __align__(16) unsigned char rows[];  // [kChunk + 1][256], the last row zero; then int [2][E]
-    __shared__ int next;
-    constexpr int C = kRowBytes / sizeof(XT), V = 16 / sizeof(XT);
-    int* cur = reinterpret_cast<int*>(rows + (kChunk + 1) * kRowBytes);
-    int* end = cur + E;
-    const int c0 = blockIdx.x * C, lane = threadIdx.x & 31, half = lane >> 4, at = lane & 15;
-    const int n = T * K, ta = blockIdx.y * per, tb = min(T, ta + per);
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-        const int q0 = min(max(offsets[e], 0), n), q1 = min(max(offsets[e + 1], q0), n);
-        cur[e] = first_at_least(slot, q0, q1, ta * K);
-    }
-    if (threadIdx.x < kRowBytes / 4) reinterpret_cast<int*>(rows + kChunk * kRowBytes)[threadIdx.x] = 0;
-    for (int t0 = ta; t0 < tb || t0 == ta; t0 += kChunk) {
-        const int t1 = min(tb, t0 + kChunk);
-        if (part) {
-            if (vec) {
+__global__ void __launch_bounds__(kThreads, 1) route_rows_kernel(const Rows a, const XT* x) {
+    // rows [chunk + 1][256], the last one zero; slots [chunk * K + E]; place [E + 1] of an expert's first slot; first [E]
+    extern __shared__ __align__(16) unsigned char rows[];
+    __shared__ int next, sums[kWarps];
+    constexpr int C = kRowBytes / sizeof(XT), V = 16 / sizeof(XT), P = 4 / sizeof(XT);  // P pairs of columns a lane
+    const int K = a.K, E = a.E, H = a.H, chunk = a.chunk;
+    SlotRef* refs = reinterpret_cast<SlotRef*>(rows + (chunk + 1) * kRowBytes);
+    int* place = reinterpret_cast<int*>(refs + chunk * K + E);
+    int* first = place + E + 1;
+    const int c0 = blockIdx.x * C, lane = threadIdx.x & 31;
+    const SlotRef none{chunk * kRowBytes, 0.0f};  // the zero row: an absent slot
+    if (threadIdx.x < kRowBytes / 4) reinterpret_cast<int*>(rows + chunk * kRowBytes)[threadIdx.x] = 0;
+    grid_wait();
+    const int k0 = blockIdx.y * a.per, k1 = min(a.n_chunks, k0 + a.per);
+    for (int k = k0; k < k1; ++k) {
+        const int t0 = k * chunk, t1 = min(a.T, t0 + chunk), ns = (t1 - t0) * K;
+        for (int e = threadIdx.x; e < E; e += kThreads) {
+            const int q0 = a.bound[k * E + e], q1 = a.bound[(k + 1) * E + e];
+            first[e] = q0;
+            place[e] = (min(max(q1 - q0, 0), ns) + 1) & ~1;  // even: two slots are read at a time
+        }
+        if (threadIdx.x == 0) next = 0;
+        // the first slots' numbers are asked for ahead of the rows: behind them they came 8000 cycles later
+        int e0[kFirst], i0[kFirst];
+        float d0[kFirst];
+#pragma unroll
+        for (int j = 0; j < kFirst; ++j) {
+            const int i = threadIdx.x + j * kThreads, at = t0 * K + i;
+            e0[j] = i < ns ? a.ids[at] : -1;
+            i0[j] = i < ns ? a.inv[at] : 0;
+            d0[j] = i < ns ? a.dl[at] : 0.0f;
+        }
+        if (a.part) {
+            if (a.vec) {
                 for (int i = threadIdx.x; i < (t1 - t0) * 16; i += kThreads) {
                     const int t = i >> 4, c = (i & 15) * V;
-                    if (c0 + c < H) cp_async16(smem_addr(rows) + i * 16, x + (size_t)(t0 + t) * ldx + c0 + c);
+                    if (c0 + c < H) cp_async16(smem_addr(rows) + i * 16, x + (size_t)(t0 + t) * a.ldx + c0 + c);
                 }
             } else {
                 for (int i = threadIdx.x; i < (t1 - t0) * C; i += kThreads) {
                     const int t = i / C, c = i % C;
-                    if (c0 + c < H) reinterpret_cast<XT*>(rows)[i] = x[(size_t)(t0 + t) * ldx + c0 + c];
+                    if (c0 + c < H) reinterpret_cast<XT*>(rows)[i] = x[(size_t)(t0 + t) * a.ldx + c0 + c];
                 }
             }
         }
-        for (int e = threadIdx.x; e < E; e += kThreads) {
-            const int q1 = min(max(offsets[e + 1], 0), n);
-            end[e] = first_at_least(slot, cur[e], max(q1, cur[e]), t1 * K);
-        }
-        if (threadIdx.x == 0) next = 0;
-        if (t0 == ta) grid_wait();  // dlogits
+        for (int i = threadIdx.x; i < ns + E; i += kThreads) refs[i] = none;
+        __syncthreads();
+        prefix(place, E, sums);
+        const int total = min(place[E], ns + E);  // (offsets that are not a plan of these slots may list too many)
+        auto put = [&](int i, int e, int q, float d) {
+            if (d == 0.0f || (unsigned)e >= (unsigned)E) return;
+            const int p = place[e] + (q - first[e]);
+            if (q >= first[e] && p >= 0 && p < place[e + 1] && p < total) refs[p] = SlotRef{i / K * kRowBytes, d};
+        };
+#pragma unroll
+        for (int j = 0; j < kFirst; ++j) put(threadIdx.x + j * kThreads, e0[j], i0[j], d0[j]);
+        for (int i = threadIdx.x + kFirst * kThreads; i < ns; i += kThreads)
+            put(i, a.ids[t0 * K + i], a.inv[t0 * K + i], a.dl[t0 * K + i]);
         cp_async_wait_all();
         __syncthreads();
         for (;;) {
@@ -203,78 +333,84 @@ __global__ void __launch_bounds__(kThreads) route_rows_kernel(const int32_t* off
             if (lane == 0) e = atomicAdd(&next, 1);  // which warp takes an expert does not show in its sum
             e = __shfl_sync(0xffffffffu, e, 0);
             if (e >= E) break;
-            const int q1 = end[e];
-            float acc[V], b = 0.0f;
+            const int q0 = min(place[e], total), q1 = min(place[e + 1], total);
+            if (a.part) {
+                float2 sum[P];
 #pragma unroll
-            for (int j = 0; j < V; ++j) acc[j] = 0.0f;
-            for (int q = cur[e]; q < q1; q += 32) {
-                int r = kChunk;  // the zero row: an absent slot, or one that is not of this chunk
-                float d = 0.0f;
-                if (q + lane < q1) {
-                    const int i = slot[q + lane];
-                    if (i >= t0 * K && i < t1 * K) {
-                        d = dl[i];
-                        if (d != 0.0f) r = i / K - t0;
+                for (int j = 0; j < P; ++j) sum[j] = make_float2(0.0f, 0.0f);
+                const unsigned char* col = rows + lane * 8;
+                auto add = [&](float f, const uint2& u) {
+                    const float2 d = make_float2(f, f);
+                    if constexpr (P == 1) {
+                        sum[0] = __ffma2_rn(d, make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), sum[0]);
+                    } else {
+                        sum[0] = __ffma2_rn(d, make_float2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u)), sum[0]);
+                        sum[P - 1] = __ffma2_rn(d, make_float2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u)), sum[P - 1]);
                     }
-                }
-                b += d;
-                if (!part) continue;
-                const int steps = (min(32, q1 - q) + 1) >> 1;
-                for (int s0 = 0; s0 < steps; s0 += 4) {
+                };
+                auto group = [&](auto pairs, int q) {  // 2 * pairs slots from q on
+                    constexpr int n = decltype(pairs)::value;
+                    int4 r[n];
+                    uint2 u[2 * n];
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {  // steps behind the last take the zero row
-                        const int src = 2 * (s0 + s) + half;
-                        const int rr = __shfl_sync(0xffffffffu, r, src);
-                        const float dd = __shfl_sync(0xffffffffu, d, src);
-                        const uint4 u = *reinterpret_cast<const uint4*>(rows + rr * kRowBytes + at * 16);
-                        if constexpr (sizeof(XT) == 4) {
-                            acc[0] = fmaf(dd, __uint_as_float(u.x), acc[0]);
-                            acc[1] = fmaf(dd, __uint_as_float(u.y), acc[1]);
-                            acc[2] = fmaf(dd, __uint_as_float(u.z), acc[2]);
-                            acc[3] = fmaf(dd, __uint_as_float(u.w), acc[3]);
-                        } else {
-                            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                    for (int s = 0; s < n; ++s) r[s] = reinterpret_cast<const int4*>(refs + q)[s];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                acc[(2 * j) % V] = fmaf(dd, __uint_as_float(w[j] << 16), acc[(2 * j) % V]);
-                                acc[(2 * j + 1) % V] = fmaf(dd, __uint_as_float(w[j] & 0xffff0000u), acc[(2 * j + 1) % V]);
-                            }
-                        }
+                    for (int s = 0; s < n; ++s) {
+                        u[2 * s] = *reinterpret_cast<const uint2*>(col + r[s].x);
+                        u[2 * s + 1] = *reinterpret_cast<const uint2*>(col + r[s].z);
                     }
+#pragma unroll
+                    for (int s = 0; s < n; ++s) {
+                        add(__int_as_float(r[s].y), u[2 * s]);
+                        add(__int_as_float(r[s].w), u[2 * s + 1]);
+                    }
+                };
+                int q = q0;
+                for (; q + 8 <= q1; q += 8) group(std::integral_constant<int, 4>(), q);
+                if (q + 4 <= q1) {
+                    group(std::integral_constant<int, 2>(), q);
+                    q += 4;
                 }
-            }
-            if (part) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 16);
-                const int c = c0 + at * V;
-                float* out = part + ((size_t)blockIdx.y * E + e) * H + c;
-                if (half == 0 && c < H) {
-                    if (vec_out) {
-#pragma unroll
-                        for (int j = 0; j < V; j += 4) {
-                            float4 v = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-                            if (t0 != ta) {
-                                const float4 o = *reinterpret_cast<const float4*>(out + j);
+                if (q < q1) group(std::integral_constant<int, 1>(), q);
+                const int c = c0 + lane * 2 * P;
+                float* out = a.part + ((size_t)blockIdx.y * E + e) * H + c;
+                const bool more = k != k0;  // added to the sums of the chunks before
+                if (c < H) {
+                    if (a.vec_out) {
+                        if constexpr (P == 2) {
+                            float4 v = make_float4(sum[0].x, sum[0].y, sum[P - 1].x, sum[P - 1].y);
+                            if (more) {
+                                const float4 o = *reinterpret_cast<const float4*>(out);
                                 v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
                             }
-                            *reinterpret_cast<float4*>(out + j) = v;
+                            *reinterpret_cast<float4*>(out) = v;
+                        } else {
+                            float2 v = sum[0];
+                            if (more) {
+                                const float2 o = *reinterpret_cast<const float2*>(out);
+                                v = make_float2(o.x + v.x, o.y + v.y);
+                            }
+                            *reinterpret_cast<float2*>(out) = v;
                         }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < V; ++j)
-                            if (c + j < H) out[j] = t0 != ta ? out[j] + acc[j] : acc[j];
+                        for (int j = 0; j < 2 * P; ++j) {
+                            const float v = j & 1 ? sum[j / 2].y : sum[j / 2].x;
+                            if (c + j < H) out[j] = more ? out[j] + v : v;
+                        }
                     }
                 }
             }
-            if (part_b && blockIdx.x == 0) {
+            if (a.part_b && blockIdx.x == 0) {
+                float b = 0.0f;
+                for (int q = q0 + lane; q < q1; q += 32) b += refs[q].d;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
-                float* out = part_b + (size_t)blockIdx.y * E + e;
-                if (lane == 0) *out = t0 != ta ? *out + b : b;
+                float* out = a.part_b + (size_t)blockIdx.y * E + e;
+                if (lane == 0) *out = k != k0 ? *out + b : b;
             }
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < E; e += kThreads) cur[e] = end[e];
     }
     grid_next();
 }
@@ -309,43 +445,61 @@ __global__ void __launch_bounds__(256) route_sum_kernel(const float* part, int s
     }
 }
 
-// Splits of the tokens: as many as fill the GPU beside the column slabs, each
-// of 128 tokens or more (the workspace's size depends on it; it must not
-// depend on the type: the fewer slabs, of bf16, count).
-struct Split {
-    int n, per;
+// How a call's tokens are cut: chunks of at most what a block's shared memory
+// holds, `per` of them to a split, `splits` splits: as many as fill the GPU
+// beside the column slabs, each of 128 tokens or more. The workspace's size
+// depends on it, so it must not depend on the type: the fewer slabs, of bf16,
+// count.
+struct Cut {
+    int chunk, n_chunks, per, splits;
 };
-Split split_of(int T, int H) {
+Cut cut_of(int T, int K, int E, int H) {
     const int slabs = (H + 127) / 128;
     int n = kSms / slabs;
     if (n > (T + 127) / 128) n = (T + 127) / 128;
     if (n < 1) n = 1;
-    const int per = T > 0 ? (T + n - 1) / n : 1;
-    return {T > 0 ? (T + per - 1) / per : 1, per};
+    Cut c;
+    const int share = T > 0 ? (T + n - 1) / n : 1, most = chunk_of(K, E);
+    c.per = (share + most - 1) / most;
+    c.chunk = (share + c.per - 1) / c.per;
+    c.n_chunks = T > 0 ? (T + c.chunk - 1) / c.chunk : 1;
+    c.splits = (c.n_chunks + c.per - 1) / c.per;
+    return c;
+}
+// The workspace: parts of drouter_w and dbias (several splits), inv, bound.
+struct Layout {
+    int64_t part_b, inv, bound, total;  // in 4-byte words
+};
+Layout layout_of(const Cut& c, int T, int K, int E, int H) {
+    auto up = [](int64_t n) { return (n + 3) / 4 * 4; };
+    Layout l;
+    l.part_b = c.splits > 1 ? up((int64_t)c.splits * E * H) : 0;
+    l.inv = l.part_b + (c.splits > 1 ? up((int64_t)c.splits * E) : 0);
+    l.bound = l.inv + up((int64_t)T * K);
+    l.total = l.bound + up((int64_t)(c.n_chunks + 1) * E);
+    return l;
 }
 
 template <typename XT>
-cudaError_t route_rows(const int32_t* offsets, const int32_t* slot, const float* dl, int T, int K, int E, const Mat& x,
-                       float* dwr, float* dbias, void* work, cudaStream_t st) {
+cudaError_t route_rows(Rows a, const Mat& x, const Cut& c, float* dwr, float* dbias, float* work, const Layout& l,
+                       cudaStream_t st) {
     constexpr int C = kRowBytes / sizeof(XT);
-    const int H = x.cols;
-    const Split sp = split_of(T, H);
-    const bool vec = x.vec() && H % (16 / sizeof(XT)) == 0;
+    const int H = a.H, E = a.E;
+    a.vec = x.vec() && H % (16 / sizeof(XT)) == 0;
     // one split writes the result itself, several their parts
-    float* part = sp.n > 1 ? (float*)work : dwr;
-    float* part_b = sp.n > 1 ? (float*)work + (size_t)sp.n * E * H : dbias;
-    const bool vec_out = H % 4 == 0 && ((uintptr_t)part & 15u) == 0 && H % (16 / sizeof(XT)) == 0;
-    const size_t smem = (size_t)(kChunk + 1) * kRowBytes + (size_t)2 * E * 4;
+    a.part = !dwr ? nullptr : c.splits > 1 ? work : dwr;
+    a.part_b = !dbias ? nullptr : c.splits > 1 ? work + l.part_b : dbias;
+    a.vec_out = H % 4 == 0 && ((uintptr_t)a.part & 15u) == 0;
+    const size_t smem = (size_t)(c.chunk + 1) * kRowBytes + ((size_t)c.chunk * a.K + E) * 8 + (size_t)(2 * E + 1) * 4;
     cudaError_t e = cudaFuncSetAttribute(route_rows_kernel<XT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    e = launch(route_rows_kernel<XT>, dim3(dwr ? (H + C - 1) / C : 1, sp.n), kThreads, smem, st, true, offsets, slot, dl, T, K,
-               E, (const XT*)x.p, x.stride, H, sp.per, vec, vec_out, dwr ? part : nullptr, dbias ? part_b : nullptr);
-    if (e != cudaSuccess || sp.n == 1) return e;
+    e = launch(route_rows_kernel<XT>, dim3(dwr ? (H + C - 1) / C : 1, c.splits), kThreads, smem, st, true, a, (const XT*)x.p);
+    if (e != cudaSuccess || c.splits == 1) return e;
     const int n = E * H;
     const bool v4 = H % 4 == 0 && (((uintptr_t)dwr | (uintptr_t)work) & 15u) == 0;
     const int V = v4 ? 4 : 1, blocks = dwr ? (n / V + 255) / 256 : 1, need = (E + 255) / 256;
     return launch(v4 ? route_sum_kernel<4> : route_sum_kernel<1>, blocks > need ? blocks : need, 256, 0, st, true,
-                  (const float*)part, sp.n, n, dwr, (const float*)part_b, E, dbias);
+                  (const float*)a.part, c.splits, n, dwr, (const float*)a.part_b, E, dbias);
 }
 
 // Columns of a slab of all E router rows (and the zero row) in shared memory.
@@ -365,10 +519,8 @@ cudaError_t route_dx(const int32_t* ids, const float* dl, const Mat& wr, int T, 
     const bool vec = H % 4 == 0 && wr.vec() && dx.vec();
     const size_t smem = (size_t)(E + 1) * C * 4;
     auto k = vc == 4 ? route_dx_kernel<XT, 4> : vc == 2 ? route_dx_kernel<XT, 2> : route_dx_kernel<XT, 1>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
     return launch(k, dim3(slabs, (T + per - 1) / per), kThreads, smem, st, true, ids, dl, (const float*)wr.p, T, K, E, H, per,
                   vec, (XT*)dx.p, dx.stride);
 }
@@ -387,8 +539,7 @@ COLI_API int64_t coli_moe_route_backward_workspace(int T, int K, int E, int H) {
     if (T < 0 || T > kBlockMaxTokens || K < 1 || K > 32 || (int64_t)T * K > kBlockMaxSlots || E < 1 || E > 1024 || H < 1 ||
         H > kBlockMaxHidden)
         return -1;
-    const int n = split_of(T, H).n;
-    return n > 1 ? (int64_t)n * E * ((int64_t)H + 1) * 4 : 0;
+    return T > 0 ? layout_of(cut_of(T, K, E, H), T, K, E, H).total * 4 : 0;
 }
 
 COLI_API coli_status coli_moe_route_backward(const float* router_w, int E, int H, int K, const void* x, coli_dtype dtype,
@@ -441,7 +592,19 @@ COLI_API coli_status coli_moe_route_backward(const float* router_w, int E, int H
         if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, (size_t)E * 4, st);
         return e == cudaSuccess ? COLI_OK : block_cuda_fail(e, "route backward: clear");
     }
-    e = launch(route_dlogits_kernel, (T + 7) / 8, 256, 0, st, false, ids, weights, dweights, T, K, E, dlogits);
+    const Cut c = cut_of(T, K, E, H);
+    const Layout l = layout_of(c, T, K, E, H);
+    Prep p{};
+    p.ids = ids, p.offsets = offsets, p.slot = slot, p.w = weights, p.dw = dweights, p.dl = dlogits;
+    p.T = T, p.K = K, p.E = E, p.chunk = c.chunk, p.n_chunks = c.n_chunks;
+    p.n_tok = (T + 7) / 8;
+    if (rows) {
+        p.inv = (int32_t*)work + l.inv;
+        p.bound = (int32_t*)work + l.bound;
+        p.n_inv = (int)(((int64_t)T * K + 255) / 256);
+    }
+    const int n_bound = rows ? ((c.n_chunks + 1) * E + 255) / 256 : 0;
+    e = launch(route_prep_kernel, p.n_tok + p.n_inv + n_bound, 256, 0, st, false, p);
     if (e != cudaSuccess) return block_cuda_fail(e, "route backward: logits");
     if (dx) {
         // few slots read fewer router rows than a slab of all of them holds
@@ -451,8 +614,12 @@ COLI_API coli_status coli_moe_route_backward(const float* router_w, int E, int H
         if (e != cudaSuccess) return block_cuda_fail(e, "route backward: dx");
     }
     if (rows) {
-        e = dtype == COLI_F32 ? route_rows<float>(offsets, slot, dlogits, T, K, E, mx, drouter_w, dbias, work, st)
-                              : route_rows<__nv_bfloat16>(offsets, slot, dlogits, T, K, E, mx, drouter_w, dbias, work, st);
+        Rows r{};
+        r.ids = ids, r.inv = p.inv, r.bound = p.bound, r.dl = dlogits;
+        r.T = T, r.K = K, r.E = E, r.H = H, r.chunk = c.chunk, r.n_chunks = c.n_chunks, r.per = c.per;
+        r.ldx = x_stride;
+        e = dtype == COLI_F32 ? route_rows<float>(r, mx, c, drouter_w, dbias, (float*)work, l, st)
+                              : route_rows<__nv_bfloat16>(r, mx, c, drouter_w, dbias, (float*)work, l, st);
         if (e != cudaSuccess) return block_cuda_fail(e, "route backward: rows");
     }
     return COLI_OK;
