@@ -173,10 +173,10 @@ __device__ __forceinline__ void ring_clear(uint32_t dst, bool all, int H) {
                 asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + (i * kParts<T> + j) * blockDim.x * 16), "r"(0)
                              : "memory");
 }
-// This thread's piece i of a row: from its ring slot (V = 8), or from memory (row: its first column's address).
-template <typename T, int V>
+// This thread's piece i of a row: from its ring slot, or from memory (row: its first column's address).
+template <typename T, int V, bool ring>
 __device__ __forceinline__ void take(Piece<T, V>& r, bool on, int i, uint32_t slot, const T* row, int H) {
-    if constexpr (V == 8) {
+    if constexpr (ring) {
 #pragma unroll
         for (int j = 0; j < kParts<T>; ++j) r.w[j] = lds16(slot + (i * kParts<T> + j) * blockDim.x * 16);
     } else {
@@ -275,7 +275,7 @@ __device__ __forceinline__ double squares64(const Piece<T, V> (&r)[N]) {
     return d;
 }
 // 1 / rms of a row held by the block.
-template <typename T, int V, int N>
+template <typename T, int V, int N, bool wide>
 __device__ __forceinline__ float row_scale(const Piece<T, V> (&r)[N], int H, float inv, float eps, float* red, double* red64) {
     float2 acc = both(0.0f);
 #pragma unroll
@@ -286,27 +286,32 @@ __device__ __forceinline__ float row_scale(const Piece<T, V> (&r)[N], int H, flo
         for (int j = 0; j < V / 2; ++j) acc = __ffma2_rn(v[j], v[j], acc);
     }
     float ss[1] = {acc.x + acc.y};
-    block_sums(ss, red);
-    if (sum_ok(ss[0], eps)) return rsqrtf(fmaf(ss[0], inv, eps));
+    if constexpr (wide) block_sum<float, 1>(ss, red);  // up to 32 warps
+    else block_sums(ss, red);
+    if (__builtin_expect(sum_ok(ss[0], eps), 1)) return rsqrtf(fmaf(ss[0], inv, eps));
     double dd[1] = {squares64<T, V, N>(r)};
     block_sum<double, 1>(dd, red64);
     return rms_scale(dd[0], H, eps);
 }
 
+// `single`: one row a block, read straight into registers by twice the threads.
+// Such a launch is as long as its code, since it runs all of it once from cold
+// instruction caches: with the ring one row of 6144 took 6.3 us, without 4.4.
 // At 2048 x 6144 bf16 (x, y, x_out, n: 101 MB) the launch bound of 80 registers
 // lets two blocks of 384 threads share an SM, one row's sums under another's copies.
-template <typename XT, typename YT, typename NT, int V, int N>
+template <typename XT, typename YT, typename NT, int V, int N, bool single>
 __global__ void __launch_bounds__(768) block_norm_kernel(const NormArgs a) {
-    __shared__ float red[2][16 * 8];
+    __shared__ float red[2][32];
     __shared__ double red64[2][32];
     extern __shared__ __align__(16) unsigned char ring_mem[];
     const int H = a.H, stages = a.stages, c0 = threadIdx.x * V;
     const bool has_prev = a.has_prev, post = a.post_norm, has_next = a.has_next;
     const float inv = 1.0f / (float)H;
-    const uint32_t xb = V == 8 ? ring_bytes<XT, N>() : 0;
-    const uint32_t slot_bytes = V == 8 ? xb + ring_bytes<YT, N>() : 0;
+    constexpr bool kRing = V == 8 && !single;
+    const uint32_t xb = kRing ? ring_bytes<XT, N>() : 0;
+    const uint32_t slot_bytes = kRing ? xb + ring_bytes<YT, N>() : 0;
     const uint32_t ring = smem_addr(ring_mem) + threadIdx.x * 16;
-    if constexpr (V == 8)
+    if constexpr (kRing)
         for (int i = 0; i < stages; ++i) {
             ring_clear<XT, N>(ring + i * slot_bytes, false, H);
             ring_clear<YT, N>(ring + i * slot_bytes + xb, !has_prev, H);
@@ -315,7 +320,7 @@ __global__ void __launch_bounds__(768) block_norm_kernel(const NormArgs a) {
     const YT* py = (const YT*)a.y + (size_t)blockIdx.x * a.ldy + c0;
     int pt = blockIdx.x;
     auto prefetch = [&](int slot) {
-        if constexpr (V == 8) {
+        if constexpr (kRing) {
             if (pt < a.T) {
                 ring_copy<XT, N>(ring + slot * slot_bytes, px, H);
                 if (has_prev) ring_copy<YT, N>(ring + slot * slot_bytes + xb, py, H);
@@ -326,7 +331,8 @@ __global__ void __launch_bounds__(768) block_norm_kernel(const NormArgs a) {
             py += a.ldy * gridDim.x;
         }
     };
-    for (int i = 0; i < (stages > 1 ? stages - 1 : 1); ++i) prefetch(i);
+    if constexpr (kRing)
+        for (int i = 0; i < (stages > 1 ? stages - 1 : 1); ++i) prefetch(i);
     float2 b[N * V / 2], q[N * V / 2];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -343,21 +349,21 @@ __global__ void __launch_bounds__(768) block_norm_kernel(const NormArgs a) {
     for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
         Piece<XT, V> rx[N];
         Piece<YT, V> ry[N];
-        if constexpr (V == 8) {
+        if constexpr (kRing) {
             cp_async_wait(stages);
             // into the slot of the row before this one, which this thread has read
             if (stages > 1) prefetch(slot == 0 ? stages - 1 : slot - 1);
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            take<XT, V>(rx[i], true, i, ring + slot * slot_bytes, (const XT*)a.x + (size_t)t * a.ldx + c0, H);
-            take<YT, V>(ry[i], has_prev, i, ring + slot * slot_bytes + xb, (const YT*)a.y + (size_t)t * a.ldy + c0, H);
+            take<XT, V, kRing>(rx[i], true, i, ring + slot * slot_bytes, (const XT*)a.x + (size_t)t * a.ldx + c0, H);
+            take<YT, V, kRing>(ry[i], has_prev, i, ring + slot * slot_bytes + xb, (const YT*)a.y + (size_t)t * a.ldy + c0, H);
         }
-        if (stages == 1) prefetch(0);
+        if (kRing && stages == 1) prefetch(0);
         slot = slot + 1 >= stages ? 0 : slot + 1;
         if (has_prev) {
             float w = a.token ? a.token[t] : 1.0f;
-            if (post) w *= row_scale<YT, V, N>(ry, H, inv, a.eps_post, red[0], red64[0]);
+            if (post) w *= row_scale<YT, V, N, single>(ry, H, inv, a.eps_post, red[0], red64[0]);
             XT* xo = (XT*)a.xo + (size_t)t * a.ldxo + c0;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -377,7 +383,7 @@ __global__ void __launch_bounds__(768) block_norm_kernel(const NormArgs a) {
             }
         }
         if (has_next) {
-            const float2 r = both(row_scale<XT, V, N>(rx, H, inv, a.eps_pre, red[1], red64[1]));
+            const float2 r = both(row_scale<XT, V, N, single>(rx, H, inv, a.eps_pre, red[1], red64[1]));
             NT* no = (NT*)a.n + (size_t)t * a.ldn + c0;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -391,6 +397,7 @@ __global__ void __launch_bounds__(768) block_norm_kernel(const NormArgs a) {
                 if (left > 0) out.store(no + i * blockDim.x * V, left);
             }
         }
+        if constexpr (single) break;
         // with one sum a row, the next row's would use the same buffer
         if (!(has_prev && post && has_next)) __syncthreads();
     }
@@ -568,10 +575,10 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
         auto row = [&](int i, int pass, float2 (&s)[P], float2 (&y)[P], float2 (&o)[P], float2 (&n)[P]) {
             const int k = V == 8 ? 0 : i;
             if (V == 8 || pass == 0) {
-                take<XT, V>(rs[k], true, i, at, (const XT*)a.x + (size_t)t * a.ldx + c0, H);
-                take<YT, V>(ry[k], has_prev, i, at + yo, (const YT*)a.y + (size_t)t * a.ldy + c0, H);
-                take<XT, V>(ro[k], has_o, i, at + oo, (const XT*)a.dxo + (size_t)t * a.lddxo + c0, H);
-                take<NT, V>(rn[k], has_next, i, at + no, (const NT*)a.dn + (size_t)t * a.lddn + c0, H);
+                take<XT, V, V == 8>(rs[k], true, i, at, (const XT*)a.x + (size_t)t * a.ldx + c0, H);
+                take<YT, V, V == 8>(ry[k], has_prev, i, at + yo, (const YT*)a.y + (size_t)t * a.ldy + c0, H);
+                take<XT, V, V == 8>(ro[k], has_o, i, at + oo, (const XT*)a.dxo + (size_t)t * a.lddxo + c0, H);
+                take<NT, V, V == 8>(rn[k], has_next, i, at + no, (const NT*)a.dn + (size_t)t * a.lddn + c0, H);
             }
             rs[k].get(s);
             ry[k].get(y);
@@ -832,6 +839,7 @@ Shape shape_of(int H, bool vec) {
 }
 
 constexpr int kSms = 148;
+constexpr int kSingleRows = kSms;  // up to here a block takes one row without the ring
 // Blocks that share an SM: as many as their registers let (80 a thread
 // forward, 128 backward), at most 8.
 int blocks_per_sm(int threads, bool fwd) {
@@ -866,13 +874,15 @@ cudaError_t launch_rows(Kernel k, NormArgs& a, const Shape& s, size_t col_bytes,
 
 template <typename XT, typename YT, typename NT>
 cudaError_t forward_typed(NormArgs& a, bool vec, cudaStream_t st) {
+    if (vec && a.T <= kSingleRows && a.H <= 8 * 768)
+        return launch(block_norm_kernel<XT, YT, NT, 8, 1, true>, a.T, (a.H / 8 + 31) / 32 * 32, 0, st, false, a);
     const Shape s = shape_of(a.H, vec);
     const Kernel k = s.N == 0   ? block_norm_wide_kernel<XT, YT, NT>
-                     : s.V == 8 ? (s.N == 1 ? block_norm_kernel<XT, YT, NT, 8, 1> : block_norm_kernel<XT, YT, NT, 8, 2>)
-                     : s.N == 1 ? block_norm_kernel<XT, YT, NT, 2, 1>
-                     : s.N == 2 ? block_norm_kernel<XT, YT, NT, 2, 2>
-                     : s.N == 4 ? block_norm_kernel<XT, YT, NT, 2, 4>
-                                : block_norm_kernel<XT, YT, NT, 2, 8>;
+                     : s.V == 8 ? (s.N == 1 ? block_norm_kernel<XT, YT, NT, 8, 1, false> : block_norm_kernel<XT, YT, NT, 8, 2, false>)
+                     : s.N == 1 ? block_norm_kernel<XT, YT, NT, 2, 1, false>
+                     : s.N == 2 ? block_norm_kernel<XT, YT, NT, 2, 2, false>
+                     : s.N == 4 ? block_norm_kernel<XT, YT, NT, 2, 4, false>
+                                : block_norm_kernel<XT, YT, NT, 2, 8, false>;
     return launch_rows(k, a, s, sizeof(XT) + sizeof(YT), s.N ? grid_of(a.T, a.H, true) : a.T, true, st);
 }
 
