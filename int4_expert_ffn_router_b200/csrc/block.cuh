@@ -56,8 +56,14 @@ struct Mat {
     // bytes from the first value to the end of the last
     size_t bytes() const { return rows > 0 ? ((size_t)(rows - 1) * stride + cols) * dtype_size(t) : 0; }
     bool aligned(size_t n) const { return ((uintptr_t)p % n) == 0; }
-    // rows start on 16-byte boundaries (one row: its start alone)
-    bool vec() const { return aligned(16) && (rows <= 1 || (size_t)stride * dtype_size(t) % 16 == 0); }
+    // rows start on n-byte boundaries (one row: its start alone)
+    bool starts(size_t n) const { return aligned(n) && (rows <= 1 || (size_t)stride * dtype_size(t) % n == 0); }
+    bool vec() const { return starts(16); }
+    // V values a thread can be read and written at a time, by accesses of up to 16 bytes
+    bool takes(int V) const {
+        const size_t n = V * dtype_size(t);
+        return cols % V == 0 && starts(n < 16 ? n : 16);
+    }
 };
 
 inline const char* check_mat(const Mat& m, const char* null_msg, const char* stride_msg, const char* align_msg) {
@@ -109,9 +115,8 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 __device__ __forceinline__ void grid_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------
-// V consecutive values of a row as fp32: V = 8 as 16-byte accesses (rows that
-// start on 16-byte boundaries and a column that is a multiple of 8), V = 1 one
-// value. The loads are volatile asm, so an in-place operator's loads and
+// V consecutive values of a row as fp32: 8, 4, 2 or 1, by accesses of up to 16
+// bytes (Mat::takes). The loads are volatile asm, so an in-place operator's loads and
 // stores keep their order.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint4 ld16(const void* p) {
@@ -167,6 +172,62 @@ struct Raw<__nv_bfloat16, 8> {
         a = make_uint4(u[0], u[1], u[2], u[3]);
     }
     __device__ __forceinline__ void store(__nv_bfloat16* p) const { st16(p, a); }
+};
+// Four or two values: rows whose starts allow 16, 8 or 4 bytes at a time.
+template <>
+struct Raw<float, 4> {
+    uint4 a;
+    __device__ __forceinline__ void load(const float* p) { a = ld16(p); }
+    __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&v)[4]) const {
+        v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+    }
+    __device__ __forceinline__ void set(const float (&v)[4]) {
+        a = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    }
+    __device__ __forceinline__ void store(float* p) const { st16(p, a); }
+};
+template <>
+struct Raw<float, 2> {
+    uint2 a;
+    __device__ __forceinline__ void load(const float* p) {
+        asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(a.x), "=r"(a.y) : "l"(p) : "memory");
+    }
+    __device__ __forceinline__ void zero() { a = make_uint2(0, 0); }
+    __device__ __forceinline__ void get(float (&v)[2]) const { v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); }
+    __device__ __forceinline__ void set(const float (&v)[2]) { a = make_uint2(__float_as_uint(v[0]), __float_as_uint(v[1])); }
+    __device__ __forceinline__ void store(float* p) const { asm volatile("st.global.v2.u32 [%0], {%1,%2};" ::"l"(p), "r"(a.x), "r"(a.y) : "memory"); }
+};
+template <>
+struct Raw<__nv_bfloat16, 4> {
+    uint2 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(a.x), "=r"(a.y) : "l"(p) : "memory");
+    }
+    __device__ __forceinline__ void zero() { a = make_uint2(0, 0); }
+    __device__ __forceinline__ void get(float (&v)[4]) const {
+        v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);
+        v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xffff0000u);
+    }
+    __device__ __forceinline__ void set(const float (&v)[4]) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[0], v[1]), l = __floats2bfloat162_rn(v[2], v[3]);
+        a = make_uint2(*reinterpret_cast<const uint32_t*>(&h), *reinterpret_cast<const uint32_t*>(&l));
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+        asm volatile("st.global.v2.u32 [%0], {%1,%2};" ::"l"(p), "r"(a.x), "r"(a.y) : "memory");
+    }
+};
+template <>
+struct Raw<__nv_bfloat16, 2> {
+    uint32_t a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { asm volatile("ld.global.u32 %0, [%1];" : "=r"(a) : "l"(p) : "memory"); }
+    __device__ __forceinline__ void zero() { a = 0; }
+    __device__ __forceinline__ void get(float (&v)[2]) const { v[0] = __uint_as_float(a << 16); v[1] = __uint_as_float(a & 0xffff0000u); }
+    __device__ __forceinline__ void set(const float (&v)[2]) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[0], v[1]);
+        a = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const { asm volatile("st.global.u32 [%0], %1;" ::"l"(p), "r"(a) : "memory"); }
 };
 template <>
 struct Raw<float, 1> {

@@ -277,32 +277,162 @@ dim3 grid_for(int T, int H, int V, int threads) {
     return dim3((unsigned)T, (unsigned)((H + V * threads - 1) / (V * threads)));
 }
 
+// The largest of 8, 4, 2 and 1 columns a thread that all these rows take.
+int columns_of(const Mat& a, const Mat& b, const Mat* c = nullptr) {
+    for (int V : {8, 4, 2})
+        if (a.takes(V) && b.takes(V) && (!c || c->takes(V))) return V;
+    return 1;
+}
+
 template <typename XT, typename RT>
 cudaError_t dispatch_rows(const Mat& x, const int32_t* pos, int T, int K, const Mat& rows, cudaStream_t st) {
-    const bool vec = x.cols % 8 == 0 && x.vec() && rows.vec();
-    const int V = vec ? 8 : 1, th = threads_for(x.cols, V);
-    return launch(vec ? dispatch_rows_kernel<XT, RT, 8> : dispatch_rows_kernel<XT, RT, 1>, grid_for(T, x.cols, V, th), th,
-                  0, st, true, (const XT*)x.p, x.stride, pos, K, x.cols, (RT*)rows.p, rows.stride);
+    const int V = columns_of(x, rows), th = threads_for(x.cols, V);
+    auto k = V == 8   ? dispatch_rows_kernel<XT, RT, 8>
+             : V == 4 ? dispatch_rows_kernel<XT, RT, 4>
+             : V == 2 ? dispatch_rows_kernel<XT, RT, 2>
+                      : dispatch_rows_kernel<XT, RT, 1>;
+    return launch(k, grid_for(T, x.cols, V, th), th, 0, st, true, (const XT*)x.p, x.stride, pos, K, x.cols, (RT*)rows.p,
+                  rows.stride);
 }
 
 template <typename RT, typename YT>
 cudaError_t gather_sum(const int32_t* pos, const float* w, int T, int K, const Mat& rows, const Mat* base, const Mat& y,
                        cudaStream_t st, bool dependent) {
-    const bool vec = y.cols % 8 == 0 && rows.vec() && y.vec() && (!base || base->vec());
-    const int V = vec ? 8 : 1, th = threads_for(y.cols, V);
-    return launch(vec ? gather_sum_kernel<RT, YT, 8> : gather_sum_kernel<RT, YT, 1>, grid_for(T, y.cols, V, th), th, 0, st,
-                  dependent, pos, w, K, (const RT*)rows.p, rows.stride, rows.rows, y.cols,
-                  (const YT*)(base ? base->p : nullptr), base ? base->stride : 0, (YT*)y.p, y.stride);
+    const int V = columns_of(rows, y, base), th = threads_for(y.cols, V);
+    auto k = V == 8   ? gather_sum_kernel<RT, YT, 8>
+             : V == 4 ? gather_sum_kernel<RT, YT, 4>
+             : V == 2 ? gather_sum_kernel<RT, YT, 2>
+                      : gather_sum_kernel<RT, YT, 1>;
+    return launch(k, grid_for(T, y.cols, V, th), th, 0, st, dependent, pos, w, K, (const RT*)rows.p, rows.stride, rows.rows,
+                  y.cols, (const YT*)(base ? base->p : nullptr), base ? base->stride : 0, (YT*)y.p, y.stride);
 }
 
 template <typename RT, typename YT>
 cudaError_t combine_backward(const int32_t* pos, const float* w, int T, int K, const Mat& dy, const Mat& rows,
                              const Mat* drows, float* dw, cudaStream_t st) {
-    const bool vec = dy.cols % 8 == 0 && dy.vec() && (!dw || rows.vec()) && (!drows || drows->vec());
-    const int V = vec ? 8 : 1;
-    return launch(vec ? combine_backward_kernel<RT, YT, 8> : combine_backward_kernel<RT, YT, 1>, T, threads_for(dy.cols, V),
-                  0, st, false, pos, w, K, (const YT*)dy.p, dy.stride, dy.cols, (const RT*)rows.p, rows.stride,
-                  rows.rows, (RT*)(drows ? drows->p : nullptr), drows ? drows->stride : 0, dw);
+    const int V = dw ? columns_of(dy, rows, drows) : columns_of(dy, *drows);
+    auto k = V == 8   ? combine_backward_kernel<RT, YT, 8>
+             : V == 4 ? combine_backward_kernel<RT, YT, 4>
+             : V == 2 ? combine_backward_kernel<RT, YT, 2>
+                      : combine_backward_kernel<RT, YT, 1>;
+    return launch(k, T, threads_for(dy.cols, V), 0, st, false, pos, w, K, (const YT*)dy.p, dy.stride, dy.cols,
+                  (const RT*)rows.p, rows.stride, rows.rows, (RT*)(drows ? drows->p : nullptr), drows ? drows->stride : 0, dw);
+}
+
+// ---------------------------------------------------------------------------
+// Few slots (decoding): one launch does all. A block takes a token and a tile
+// of columns, and finds the rows of its K slots by comparing them with every
+// slot: row = number of slots of lower experts, and of the same expert before
+// it. The last block writes the counts, the offsets and the slots' tail. One
+// launch costs the caller 2 us less than two.
+// ---------------------------------------------------------------------------
+constexpr int kFewSlots = 1024;
+constexpr int kFewThreads = 256;
+
+struct Few {
+    const int32_t* ids;
+    int T, K, E, H, move;
+    int64_t ldx, ldr;
+    int32_t *counts, *offsets, *pos, *slot;
+};
+
+template <typename XT, typename RT, int V>
+__global__ void __launch_bounds__(kFewThreads) dispatch_few_kernel(const Few a, const XT* x, RT* rows) {
+    constexpr int kEach = kFewSlots / kFewThreads;
+    __shared__ int32_t found[32][kFewThreads / 32];
+    __shared__ int32_t hist[1024], sums[32];
+    const int n = a.T * a.K, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = blockIdx.x, c = (blockIdx.y * kFewThreads + threadIdx.x) * V;
+    int32_t e[kEach];  // slots threadIdx.x, + 256, ..; E: an empty slot
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        const int i = threadIdx.x + j * kFewThreads;
+        const int id = i < n ? a.ids[i] : a.E;
+        e[j] = (unsigned)id < (unsigned)a.E ? id : a.E;
+    }
+    if (t == a.T) {
+        if (blockIdx.y) return;
+        for (int i = threadIdx.x; i < a.E; i += kFewThreads) hist[i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+            if (e[j] < a.E) atomicAdd(hist + e[j], 1);  // an integer count: the order does not matter
+        __syncthreads();
+        int v[4], own = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = threadIdx.x * 4 + j;
+            v[j] = i < a.E ? hist[i] : 0;
+            own += v[j];
+        }
+        int s = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += u;
+        }
+        if (lane == 31) sums[warp] = s;
+        __syncthreads();
+        int off = s - own, all = 0;
+        for (int w = 0; w < kFewThreads / 32; ++w) {
+            if (w < warp) off += sums[w];
+            all += sums[w];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = threadIdx.x * 4 + j;
+            if (i < a.E) {
+                a.counts[i] = v[j];
+                a.offsets[i] = off;
+            }
+            off += v[j];
+        }
+        if (threadIdx.x == 0) a.offsets[a.E] = all;
+        for (int i = all + threadIdx.x; i < n; i += kFewThreads) a.slot[i] = -1;
+        return;
+    }
+    Raw<XT, V> in;
+    in.zero();
+    if (a.move && c < a.H) in.load(x + (size_t)t * a.ldx + c);
+    for (int k = 0; k < a.K; ++k) {
+        const int i = t * a.K + k, id = a.ids[i];
+        int before = 0;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            const int at = threadIdx.x + j * kFewThreads;
+            before += e[j] < id || (e[j] == id && at < i);
+        }
+        before = __reduce_add_sync(0xffffffffu, before);
+        if (lane == 0) found[k][warp] = before;
+    }
+    __syncthreads();
+    float f[V];
+    in.get(f);
+    Raw<RT, V> out;
+    out.set(f);
+    for (int k = 0; k < a.K; ++k) {
+        const int i = t * a.K + k, id = a.ids[i];
+        const bool held = (unsigned)id < (unsigned)a.E;
+        int q = 0;
+#pragma unroll
+        for (int w = 0; w < kFewThreads / 32; ++w) q += found[k][w];
+        if (held && a.move && c < a.H) out.store(rows + (size_t)q * a.ldr + c);
+        if (blockIdx.y == 0 && threadIdx.x == 0) {
+            a.pos[i] = held ? q : -1;
+            if (held) a.slot[q] = i;
+        }
+    }
+}
+
+template <typename XT, typename RT>
+cudaError_t dispatch_few(const Few& a, const Mat& x, const Mat& rows, cudaStream_t st) {
+    const int V = a.move ? columns_of(x, rows) : 8;
+    auto k = V == 8   ? dispatch_few_kernel<XT, RT, 8>
+             : V == 4 ? dispatch_few_kernel<XT, RT, 4>
+             : V == 2 ? dispatch_few_kernel<XT, RT, 2>
+                      : dispatch_few_kernel<XT, RT, 1>;
+    const int tiles = a.move ? (a.H + V * kFewThreads - 1) / (V * kFewThreads) : 1;
+    return launch(k, dim3(a.T + 1, tiles), kFewThreads, 0, st, false, a, (const XT*)x.p, (RT*)rows.p);
 }
 
 const char* check_slots(int T, int K) {
@@ -420,6 +550,15 @@ COLI_API coli_status coli_moe_dispatch(const int32_t* ids, int T, int K, int E, 
     cudaStream_t st = (cudaStream_t)stream;
     const Chunks c = chunks_of((int64_t)n);
     cudaError_t e = cudaSuccess;
+    using B = __nv_bfloat16;
+    if (n <= kFewSlots) {
+        const Few f{ids, T, K, E, hidden, move, x_stride, rows_stride, counts, offsets, pos, slot};
+        if (!move || x_dtype == COLI_F32)
+            e = !move || rows_dtype == COLI_F32 ? dispatch_few<float, float>(f, mx, mr, st) : dispatch_few<float, B>(f, mx, mr, st);
+        else
+            e = rows_dtype == COLI_F32 ? dispatch_few<B, float>(f, mx, mr, st) : dispatch_few<B, B>(f, mx, mr, st);
+        return e == cudaSuccess ? COLI_OK : block_cuda_fail(e, "dispatch");
+    }
     if (c.n > 1)
         e = launch(dispatch_count_kernel, c.n, kRankThreads, 0, st, false, ids, (int)n, E, c.size, (int32_t*)work);
     if (e != cudaSuccess) return block_cuda_fail(e, "dispatch: count");
@@ -432,7 +571,6 @@ COLI_API coli_status coli_moe_dispatch(const int32_t* ids, int T, int K, int E, 
                counts, offsets, pos, slot);
     if (e != cudaSuccess) return block_cuda_fail(e, "dispatch: rank");
     if (!move) return COLI_OK;
-    using B = __nv_bfloat16;
     if (x_dtype == COLI_F32)
         e = rows_dtype == COLI_F32 ? dispatch_rows<float, float>(mx, pos, T, K, mr, st)
                                    : dispatch_rows<float, B>(mx, pos, T, K, mr, st);
