@@ -91,23 +91,34 @@ inline bool overlap(const Mat& a, const Mat& b) {
 // The same matrix (an operator that reads each value before it writes it takes this).
 inline bool same(const Mat& a, const Mat& b) { return a.p == b.p && a.t == b.t && a.stride == b.stride; }
 
-// Launches `kernel`. dependent: it may start while the kernel before it on the
-// stream still runs, and waits for that one's results itself (grid_wait).
+// Launches `kernel`, in clusters of `cluster` blocks. dependent: it may start
+// while the kernel before it on the stream still runs, and waits for that one's
+// results itself (grid_wait).
 template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, bool dependent, A... args) {
+cudaError_t launch_clusters(int cluster, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                            bool dependent, A... args) {
     cudaLaunchConfig_t c{};
     c.gridDim = grid;
     c.blockDim = block;
     c.dynamicSmemBytes = smem;
     c.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
+    c.attrs = at;
     if (dependent) {
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
-        c.attrs = at;
-        c.numAttrs = 1;
+        at[c.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[c.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        at[c.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        at[c.numAttrs].val.clusterDim.x = cluster;
+        at[c.numAttrs].val.clusterDim.y = 1;
+        at[c.numAttrs++].val.clusterDim.z = 1;
     }
     return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+}
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, bool dependent, A... args) {
+    return launch_clusters(1, kernel, grid, block, smem, st, dependent, args...);
 }
 // Waits until the kernels before this one have finished and their writes can be read.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

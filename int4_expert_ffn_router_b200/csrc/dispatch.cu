@@ -99,18 +99,15 @@ __global__ void __launch_bounds__(kRankThreads) dispatch_rank_kernel(const int32
             mine += v;
         }
     }
-    int total = mine, before = 0;  // over all chunks; over the chunks before this one
-    if (gridDim.x > 1) {
-        grid_wait();
-        total = 0;
-        if (threadIdx.x < E)
+    int total = 0, before = 0;  // over all chunks; over the chunks before this one
+    grid_wait();
+    if (threadIdx.x < E)
 #pragma unroll 8
-            for (int b = 0; b < (int)gridDim.x; ++b) {
-                const int v = hist[(size_t)b * E + threadIdx.x];
-                if (b < (int)blockIdx.x) before += v;
-                total += v;
-            }
-    }
+        for (int b = 0; b < (int)gridDim.x; ++b) {
+            const int v = hist[(size_t)b * E + threadIdx.x];
+            if (b < (int)blockIdx.x) before += v;
+            total += v;
+        }
     int all;
     const int off = block_scan(total, sums, &all);
     if (threadIdx.x < E) {
@@ -143,6 +140,109 @@ __global__ void __launch_bounds__(kRankThreads) dispatch_rank_kernel(const int32
 }
 
 size_t rank_smem(int E) { return sizeof(int32_t) * ((size_t)kRankWarps * E + 32); }
+
+// ---------------------------------------------------------------------------
+// The same sort in one launch for up to kClusterSlots slots: a cluster of eight
+// blocks, a chunk each, which read each other's counts from shared memory. A
+// warp's first 64 slots stay in registers between the two passes. 16384 slots
+// of 256 experts took the two launches above 10 us, this one 5 (and the rows
+// kernel starts meanwhile).
+// ---------------------------------------------------------------------------
+constexpr int kCluster = 8;
+constexpr int kClusterSlots = 1 << 17;
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// A word of block `rank`'s shared memory, at the place that `p` has in this block's.
+__device__ __forceinline__ int32_t cluster_read(const int32_t* p, int rank) {
+    uint32_t a;
+    int32_t v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+__global__ void __launch_bounds__(kRankThreads, 1) dispatch_sort_kernel(const int32_t* ids, int n, int E, int chunk,
+                                                                        int32_t* counts, int32_t* offsets, int32_t* pos,
+                                                                        int32_t* slot) {
+    extern __shared__ int32_t sh[];  // wcnt [kRankWarps][E], tot [E], sums [32]
+    int32_t *wcnt = sh, *tot = sh + kRankWarps * E, *sums = tot + E;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = blockIdx.x;
+    grid_next();  // the rows kernel may start: it waits for this one's end itself
+    const int c0 = min(n, rank * chunk), c1 = min(n, c0 + chunk), per = chunk / kRankWarps;
+    const int w0 = c0 + warp * per, w1 = min(c1, w0 + per);
+    auto fetch = [&](int i) {
+        const int e = i < w1 ? ids[i] : -1;
+        return (unsigned)e < (unsigned)E ? e : -1;
+    };
+    int kept[2];
+    kept[0] = fetch(w0 + lane);
+    kept[1] = fetch(w0 + 32 + lane);
+    for (int i = threadIdx.x; i < kRankWarps * E; i += kRankThreads) wcnt[i] = 0;
+    __syncthreads();
+    auto count = [&](int e) {
+        const unsigned m = __match_any_sync(0xffffffffu, e);
+        if (e >= 0 && lane == __ffs(m) - 1) wcnt[warp * E + e] += __popc(m);
+        __syncwarp();
+    };
+    count(kept[0]);
+    if (per > 32) count(kept[1]);
+    for (int i0 = w0 + 64; i0 < w0 + per; i0 += 32) count(fetch(i0 + lane));
+    __syncthreads();
+    int mine = 0, c[kRankWarps];
+    if (threadIdx.x < E) {
+#pragma unroll
+        for (int w = 0; w < kRankWarps; ++w) c[w] = wcnt[w * E + threadIdx.x];
+#pragma unroll
+        for (int w = 0; w < kRankWarps; ++w) {
+            const int v = c[w];
+            c[w] = mine;
+            mine += v;
+        }
+        tot[threadIdx.x] = mine;
+    }
+    cluster_arrive();
+    cluster_wait();
+    int total = 0, before = 0;  // over all chunks; over the chunks before this one
+    if (threadIdx.x < E) {
+#pragma unroll
+        for (int b = 0; b < kCluster; ++b) {
+            const int v = cluster_read(tot + threadIdx.x, b);
+            if (b < rank) before += v;
+            total += v;
+        }
+    }
+    cluster_arrive();  // (no block leaves before the others have read its counts)
+    int all;
+    const int off = block_scan(total, sums, &all);
+    if (threadIdx.x < E) {
+#pragma unroll
+        for (int w = 0; w < kRankWarps; ++w) wcnt[w * E + threadIdx.x] = c[w] + off + before;
+        if (rank == 0) {
+            counts[threadIdx.x] = total;
+            offsets[threadIdx.x] = off;
+        }
+    }
+    if (rank == 0 && threadIdx.x == 0) offsets[E] = all;
+    __syncthreads();
+    auto place = [&](int i, int e) {
+        const unsigned m = __match_any_sync(0xffffffffu, e);
+        int q = -1;
+        if (e >= 0) {
+            q = wcnt[warp * E + e] + __popc(m & ((1u << lane) - 1u));
+            slot[q] = i;
+        }
+        if (i < w1) pos[i] = q;
+        __syncwarp();
+        if (e >= 0 && lane == __ffs(m) - 1) wcnt[warp * E + e] += __popc(m);
+        __syncwarp();
+    };
+    place(w0 + lane, kept[0]);
+    if (per > 32) place(w0 + 32 + lane, kept[1]);
+    for (int i0 = w0 + 64; i0 < w0 + per; i0 += 32) place(i0 + lane, fetch(i0 + lane));
+    for (int i = max(c0, all) + threadIdx.x; i < c1; i += kRankThreads) slot[i] = -1;  // behind the last expert
+    cluster_wait();
+}
 
 // rows[pos[t][k]] = x[t]: a thread reads V columns of a token once and writes
 // them K times. Bound by the K rows a token writes.
@@ -508,8 +608,8 @@ using namespace coli;
 
 COLI_API int64_t coli_moe_dispatch_workspace(int T, int K, int E) {
     if (check_slots(T, K) || E < 1 || E > 1024) return -1;
-    const Chunks c = chunks_of((int64_t)T * K);
-    return c.n > 1 ? (int64_t)c.n * E * 4 : 0;
+    const int64_t n = (int64_t)T * K;
+    return n > kClusterSlots ? (int64_t)chunks_of(n).n * E * 4 : 0;
 }
 
 COLI_API coli_status coli_moe_dispatch(const int32_t* ids, int T, int K, int E, const void* x, coli_dtype x_dtype,
@@ -559,17 +659,24 @@ COLI_API coli_status coli_moe_dispatch(const int32_t* ids, int T, int K, int E, 
             e = rows_dtype == COLI_F32 ? dispatch_few<B, float>(f, mx, mr, st) : dispatch_few<B, B>(f, mx, mr, st);
         return e == cudaSuccess ? COLI_OK : block_cuda_fail(e, "dispatch");
     }
-    if (c.n > 1)
+    if (n <= kClusterSlots) {
+        const int chunk = (int)((n + kCluster * kRankThreads - 1) / (kCluster * kRankThreads)) * kRankThreads;
+        const size_t smem = rank_smem(E) + (size_t)E * 4;
+        e = cudaFuncSetAttribute(dispatch_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return block_cuda_fail(e, "dispatch: shared memory");
+        e = launch_clusters(kCluster, dispatch_sort_kernel, kCluster, kRankThreads, smem, st, false, ids, (int)n, E, chunk,
+                            counts, offsets, pos, slot);
+        if (e != cudaSuccess) return block_cuda_fail(e, "dispatch: sort");
+    } else {
         e = launch(dispatch_count_kernel, c.n, kRankThreads, 0, st, false, ids, (int)n, E, c.size, (int32_t*)work);
-    if (e != cudaSuccess) return block_cuda_fail(e, "dispatch: count");
-    const size_t smem = rank_smem(E);
-    if (smem > 48 * 1024) {
+        if (e != cudaSuccess) return block_cuda_fail(e, "dispatch: count");
+        const size_t smem = rank_smem(E);
         e = cudaFuncSetAttribute(dispatch_rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return block_cuda_fail(e, "dispatch: shared memory");
+        e = launch(dispatch_rank_kernel, c.n, kRankThreads, smem, st, true, ids, (int)n, E, c.size, (const int32_t*)work,
+                   counts, offsets, pos, slot);
+        if (e != cudaSuccess) return block_cuda_fail(e, "dispatch: rank");
     }
-    e = launch(dispatch_rank_kernel, c.n, kRankThreads, smem, st, c.n > 1, ids, (int)n, E, c.size, (const int32_t*)work,
-               counts, offsets, pos, slot);
-    if (e != cudaSuccess) return block_cuda_fail(e, "dispatch: rank");
     if (!move) return COLI_OK;
     if (x_dtype == COLI_F32)
         e = rows_dtype == COLI_F32 ? dispatch_rows<float, float>(mx, pos, T, K, mr, st)

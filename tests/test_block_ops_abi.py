@@ -58,9 +58,9 @@ def _dispatch(coli, **kw):
     (dict(xs=63), "x_stride"), (dict(rs=0), "rows_stride"), (dict(n_rows=7), "n_rows"), (dict(x=P[1] + 2), "aligned"),
     (dict(rows=P[6] + 1), "aligned"), (dict(ids=P[0] + 2), "4-byte"), (dict(rows=P[1] + 64), "overlap"),
     (dict(pos=P[0]), "overlap"), (dict(counts=P[3] + 4), "overlap"), (dict(slot=P[1] + 16), "overlap"),
-    (dict(dev=-1), "device"), (dict(T=2048, K=8, n_rows=1 << 14), "work"),
-    (dict(T=2048, K=8, n_rows=1 << 14, work=P[7], nw=511), "work"),
-    (dict(T=2048, K=8, n_rows=1 << 14, work=P[7] + 8, nw=1 << 20), "16-byte"),
+    (dict(dev=-1), "device"), (dict(T=40000, K=8, n_rows=1 << 19), "work"),
+    (dict(T=40000, K=8, n_rows=1 << 19, work=P[7], nw=511), "work"),
+    (dict(T=40000, K=8, n_rows=1 << 19, work=P[7] + 8, nw=1 << 20), "16-byte"),
 ])
 def test_dispatch_refuses(coli, kw, msg):
     st, err = _dispatch(coli, **kw)

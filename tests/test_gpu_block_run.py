@@ -141,7 +141,7 @@ def test_captured_and_replayed(gpu, coli):
             assert torch.equal(v, getattr(m, k)), k
 
 
-@pytest.mark.parametrize("T", [7, 1500])
+@pytest.mark.parametrize("T", [7, 1500, 17000])
 def test_large_plan_captured(gpu, coli, T):
     """The sort's several launches in a graph, back to back with another call's on the same workspace."""
     K, E, H = 8, 64, 128

@@ -55,7 +55,7 @@ def run_plan(coli, ids, E, dev, x=None, rows=None):
 
 PLANS = [(1, 1, 1, "random"), (1, 8, 256, "random"), (3, 2, 16, "holes"), (5, 32, 32, "random"), (64, 8, 256, "random"),
          (127, 8, 256, "one"), (33, 4, 7, "none"), (256, 8, 256, "holes"), (257, 8, 256, "random"), (1000, 6, 64, "holes"),
-         (2048, 8, 256, "random"), (2049, 8, 1024, "holes"), (5000, 8, 300, "one"), (70000, 3, 1024, "random")]
+         (2048, 8, 256, "random"), (2049, 8, 1024, "holes"), (5000, 8, 300, "one"), (70000, 3, 1024, "random"), (16385, 8, 64, "holes")]
 
 
 @pytest.mark.parametrize("T,K,E,kind", PLANS)
