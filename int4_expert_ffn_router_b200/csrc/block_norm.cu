@@ -316,34 +316,33 @@ __global__ void __launch_bounds__(768) block_norm_kernel(const NormArgs a) {
             ring_clear<XT, N>(ring + i * slot_bytes, false, H);
             ring_clear<YT, N>(ring + i * slot_bytes + xb, !has_prev, H);
         }
-    const XT* px = (const XT*)a.x + (size_t)blockIdx.x * a.ldx + c0;  // this thread's first column of the next row to copy
-    const YT* py = (const YT*)a.y + (size_t)blockIdx.x * a.ldy + c0;
-    int pt = blockIdx.x;
+    int pt = blockIdx.x;  // the next row to copy
     auto prefetch = [&](int slot) {
         if constexpr (kRing) {
             if (pt < a.T) {
-                ring_copy<XT, N>(ring + slot * slot_bytes, px, H);
-                if (has_prev) ring_copy<YT, N>(ring + slot * slot_bytes + xb, py, H);
+                ring_copy<XT, N>(ring + slot * slot_bytes, (const XT*)a.x + (size_t)pt * a.ldx + c0, H);
+                if (has_prev) ring_copy<YT, N>(ring + slot * slot_bytes + xb, (const YT*)a.y + (size_t)pt * a.ldy + c0, H);
             }
             cp_async_commit();
             pt += gridDim.x;
-            px += a.ldx * gridDim.x;
-            py += a.ldy * gridDim.x;
         }
     };
-    if constexpr (kRing)
-        for (int i = 0; i < (stages > 1 ? stages - 1 : 1); ++i) prefetch(i);
     float2 b[N * V / 2], q[N * V / 2];
+    // one row's copies, then the parameters (they would wait behind a full ring), then the other slots'
+    for (int k = 0; k == 0 || k < stages - 1; ++k) {
+        prefetch(k);
+        if (k) continue;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
-        float2 f[V / 2];
-        if (has_prev) load_branch<V>(a, c, f);
+        for (int i = 0; i < N; ++i) {
+            const int c = (i * blockDim.x + threadIdx.x) * V;
+            float2 f[V / 2];
+            if (has_prev) load_branch<V>(a, c, f);
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) b[i * V / 2 + j] = f[j];
-        if (has_next) load_columns<V>(a.pre, c, H, f);
+            for (int j = 0; j < V / 2; ++j) b[i * V / 2 + j] = f[j];
+            if (has_next) load_columns<V>(a.pre, c, H, f);
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) q[i * V / 2 + j] = f[j];
+            for (int j = 0; j < V / 2; ++j) q[i * V / 2 + j] = f[j];
+        }
     }
     int slot = 0;
     for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
@@ -542,9 +541,10 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
             pt += gridDim.x;
         }
     };
-    for (int i = 0; i < (stages > 1 ? stages - 1 : 1); ++i) prefetch(i);
+    grid_next();  // sum_parts_kernel may start: it waits for this one's end itself
     constexpr int P = V / 2;
     float2 b[N * P], q[N * P], dq[N * P], A[N * P];
+    prefetch(0);  // one row, then the parameters: behind a full ring (21 MB) they came 3 us later
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * V;
@@ -556,6 +556,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
 #pragma unroll
         for (int j = 0; j < P; ++j) b[i * P + j] = f[j], q[i * P + j] = g[j], dq[i * P + j] = A[i * P + j] = both(0.0f);
     }
+    for (int i = 1; i < stages - 1; ++i) prefetch(i);
     int slot = 0, flip = 0;
     const float inv = 1.0f / (float)H;
     const bool tiny_s = has_next && a.eps_pre < 1e-12f, tiny_y = post && a.eps_post < 1e-12f;  // see sum_ok
@@ -692,15 +693,26 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
         for (int i = 0; i < N; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * V;
             float* out = a.part + (size_t)blockIdx.x * 2 * H + c;
+            if constexpr (V == 8) {
+                if (c >= H) continue;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                if (c + j >= H) break;
-                out[j] = j & 1 ? dq[i * P + j / 2].y : dq[i * P + j / 2].x;
-                out[(size_t)H + j] = j & 1 ? A[i * P + j / 2].y : A[i * P + j / 2].x;
+                for (int j = 0; j < P; j += 2) {
+                    const float2 x0 = dq[i * P + j], x1 = dq[i * P + j + 1], y0 = A[i * P + j], y1 = A[i * P + j + 1];
+                    *reinterpret_cast<float4*>(out + 2 * j) = make_float4(x0.x, x0.y, x1.x, x1.y);
+                    *reinterpret_cast<float4*>(out + H + 2 * j) = make_float4(y0.x, y0.y, y1.x, y1.y);
+                }
+            } else {
+                if (c < H) {
+                    out[0] = dq[i].x;
+                    out[H] = A[i].x;
+                }
+                if (c + 1 < H) {
+                    out[1] = dq[i].y;
+                    out[H + 1] = A[i].y;
+                }
             }
         }
     }
-    grid_next();
 }
 
 // Rows too wide for registers: the columns are read again in each round, and
