@@ -809,22 +809,26 @@ __global__ void __launch_bounds__(1024) block_norm_backward_wide_kernel(NormArgs
 }
 
 // The gains' and the gate's gradients from the blocks' sums, added in block
-// order: 32 columns and 8 runs of blocks a block.
-__global__ void __launch_bounds__(256) sum_parts_kernel(const NormArgs a, int n, float* dpre, float* dpost, float* dgate) {
-    __shared__ float sh[8][32];
+// order: 32 columns and 16 runs of blocks a block, ten loads of a run in flight.
+__global__ void __launch_bounds__(512) sum_parts_kernel(const NormArgs a, int n, float* dpre, float* dpost, float* dgate) {
+    __shared__ float sh[16][32];
     grid_wait();
     const int H = a.H, which = blockIdx.y, c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
     if (which == 0 ? !dpre : !dpost && !dgate) return;
-    const int per = (n + 7) / 8, b0 = g * per, b1 = min(n, b0 + per);
+    const int per = (n + 15) / 16, b0 = g * per, b1 = min(n, b0 + per);
     float acc = 0.0f;
-    if (c < H)
-#pragma unroll 8
-        for (int b = b0; b < b1; ++b) acc += __ldcg(a.part + ((size_t)b * 2 + which) * H + c);
+    for (int b = b0; b < b1 && c < H; b += 10) {
+        float v[10];
+#pragma unroll
+        for (int j = 0; j < 10; ++j) v[j] = b + j < b1 ? __ldcg(a.part + ((size_t)(b + j) * 2 + which) * H + c) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 10; ++j) acc += v[j];
+    }
     sh[g][threadIdx.x & 31] = acc;
     __syncthreads();
     if (g != 0 || c >= H) return;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) acc += sh[i][threadIdx.x];
+    for (int i = 1; i < 16; ++i) acc += sh[i][threadIdx.x];
     if (which == 0) {
         dpre[c] = acc;
         return;
@@ -1150,6 +1154,6 @@ COLI_API coli_status coli_block_norm_backward(const coli_block_params* prev, con
         if (e != cudaSuccess) return block_cuda_fail(e, "block norm backward");
     }
     if (!want) return COLI_OK;
-    e = launch(sum_parts_kernel, dim3((H + 31) / 32, 2), 256, 0, s, T > 0, a, grid_of(T, H, false), dpre_gain, dpost_gain, dgate);
+    e = launch(sum_parts_kernel, dim3((H + 31) / 32, 2), 512, 0, s, T > 0, a, grid_of(T, H, false), dpre_gain, dpost_gain, dgate);
     return e == cudaSuccess ? COLI_OK : block_cuda_fail(e, "block norm backward: gains");
 }
