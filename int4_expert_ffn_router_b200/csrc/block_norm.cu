@@ -557,6 +557,22 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
         for (int j = 0; j < P; ++j) b[i * P + j] = f[j], q[i * P + j] = g[j], dq[i * P + j] = A[i * P + j] = both(0.0f);
     }
     for (int i = 1; i < stages - 1; ++i) prefetch(i);
+    // V = 2: the next row's columns are loaded while a row is worked on, where the registers allow it
+    constexpr bool kAhead = V == 2 && N <= 4;
+    constexpr int kKept = V == 8 ? 1 : N;
+    Piece<XT, V> rs[kKept], ro[kKept];
+    Piece<YT, V> ry[kKept];
+    Piece<NT, V> rn[kKept];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < kKept; ++i) {
+            take<XT, V, false>(rs[i], true, i, 0, (const XT*)a.x + (size_t)t * a.ldx + c0, H);
+            take<YT, V, false>(ry[i], has_prev, i, 0, (const YT*)a.y + (size_t)t * a.ldy + c0, H);
+            take<XT, V, false>(ro[i], has_o, i, 0, (const XT*)a.dxo + (size_t)t * a.lddxo + c0, H);
+            take<NT, V, false>(rn[i], has_next, i, 0, (const NT*)a.dn + (size_t)t * a.lddn + c0, H);
+        }
+    };
+    if constexpr (kAhead) fetch(blockIdx.x);
     int slot = 0, flip = 0;
     const float inv = 1.0f / (float)H;
     const bool tiny_s = has_next && a.eps_pre < 1e-12f, tiny_y = post && a.eps_post < 1e-12f;  // see sum_ok
@@ -568,23 +584,35 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
         }
         const uint32_t at = ring + slot * slot_bytes;
         slot = slot + 1 >= stages ? 0 : slot + 1;
-        // Wide pieces are read from the ring in every pass over the row; single columns stay in registers.
-        constexpr int kKept = V == 8 ? 1 : N;
-        Piece<XT, V> rs[kKept], ro[kKept];
-        Piece<YT, V> ry[kKept];
-        Piece<NT, V> rn[kKept];
-        auto row = [&](int i, int pass, float2 (&s)[P], float2 (&y)[P], float2 (&o)[P], float2 (&n)[P]) {
-            const int k = V == 8 ? 0 : i;
-            if (V == 8 || pass == 0) {
-                take<XT, V, V == 8>(rs[k], true, i, at, (const XT*)a.x + (size_t)t * a.ldx + c0, H);
-                take<YT, V, V == 8>(ry[k], has_prev, i, at + yo, (const YT*)a.y + (size_t)t * a.ldy + c0, H);
-                take<XT, V, V == 8>(ro[k], has_o, i, at + oo, (const XT*)a.dxo + (size_t)t * a.lddxo + c0, H);
-                take<NT, V, V == 8>(rn[k], has_next, i, at + no, (const NT*)a.dn + (size_t)t * a.lddn + c0, H);
+        // Wide pieces are read from the ring in every pass over the row; single columns stay in registers
+        // (as values where the next row's are being loaded).
+        float2 ks[kAhead ? N : 1], ky[kAhead ? N : 1], ko[kAhead ? N : 1], kn[kAhead ? N : 1];
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                rs[i].get(reinterpret_cast<float2(&)[P]>(ks[i]));
+                ry[i].get(reinterpret_cast<float2(&)[P]>(ky[i]));
+                ro[i].get(reinterpret_cast<float2(&)[P]>(ko[i]));
+                rn[i].get(reinterpret_cast<float2(&)[P]>(kn[i]));
             }
-            rs[k].get(s);
-            ry[k].get(y);
-            ro[k].get(o);
-            rn[k].get(n);
+            if (t + (int)gridDim.x < a.T) fetch(t + gridDim.x);
+        }
+        auto row = [&](int i, int pass, float2 (&s)[P], float2 (&y)[P], float2 (&o)[P], float2 (&n)[P]) {
+            if constexpr (kAhead) {
+                s[0] = ks[i], y[0] = ky[i], o[0] = ko[i], n[0] = kn[i];
+            } else {
+                const int k = V == 8 ? 0 : i;
+                if (V == 8 || pass == 0) {
+                    take<XT, V, V == 8>(rs[k], true, i, at, (const XT*)a.x + (size_t)t * a.ldx + c0, H);
+                    take<YT, V, V == 8>(ry[k], has_prev, i, at + yo, (const YT*)a.y + (size_t)t * a.ldy + c0, H);
+                    take<XT, V, V == 8>(ro[k], has_o, i, at + oo, (const XT*)a.dxo + (size_t)t * a.lddxo + c0, H);
+                    take<NT, V, V == 8>(rn[k], has_next, i, at + no, (const NT*)a.dn + (size_t)t * a.lddn + c0, H);
+                }
+                rs[k].get(s);
+                ry[k].get(y);
+                ro[k].get(o);
+                rn[k].get(n);
+            }
         };
         const float u = a.token ? a.token[t] : 1.0f;
         float2 acc[6];
