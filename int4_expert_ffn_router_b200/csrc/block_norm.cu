@@ -2,6 +2,8 @@
 // (coli_block_norm) and their gradients.
 #include "block.cuh"
 
+#include <initializer_list>
+
 #define COLI_API extern "C" __attribute__((visibility("default")))
 
 namespace coli {
@@ -47,13 +49,15 @@ __device__ __forceinline__ void load_gain(const float* g, int c, float (&v)[V]) 
 }
 
 // ---------------------------------------------------------------------------
-// A thread holds N pieces of V columns of a row: V = 8 with 16-byte accesses
-// (rows that start on 16-byte boundaries, H % 8 == 0), else V = 2 read one by
-// one. Arithmetic is on pairs of columns (fp32 x 2 instructions): a row's
+// A thread holds N pieces of V columns of a row: V = 8 where all rows are bf16,
+// V = 4 where some are fp32 (so that a warp's 16-byte accesses lie side by side:
+// two of them 32 bytes apart read every 32-byte sector twice, and took 1.6 times
+// as long), both for rows whose starts allow it; else V = 2, read one by one.
+// Arithmetic is on pairs of columns (fp32 x 2 instructions): a row's
 // instructions, not its bytes, bound these kernels otherwise.
 //
 // A block takes the rows b, b + grid, ...: the columns' parameters are read
-// once, and with V = 8 the next rows are copied into a ring in shared memory
+// once, and with V >= 4 the next rows are copied into a ring in shared memory
 // (cp.async) while a row is worked on. A thread copies what it alone reads, so
 // the ring needs no barrier.
 // ---------------------------------------------------------------------------
@@ -66,40 +70,64 @@ __device__ __forceinline__ uint32_t to_bf16_pair(float2 v) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ uint2 ld8(const void* p) {
+    uint2 r;
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+    uint2 r;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a) : "memory");
+    return r;
+}
+
 template <typename T, int V>
 struct Piece;
 template <>
-struct Piece<float, 8> {
-    uint4 w[2];
-    __device__ __forceinline__ void zero() { w[0] = w[1] = make_uint4(0, 0, 0, 0); }
+struct Piece<__nv_bfloat16, 8> {
+    uint4 w;
+    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void get(float2 (&v)[4]) const {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            v[2 * i] = make_float2(__uint_as_float(w[i].x), __uint_as_float(w[i].y));
-            v[2 * i + 1] = make_float2(__uint_as_float(w[i].z), __uint_as_float(w[i].w));
-        }
+        v[0] = bf16_pair(w.x); v[1] = bf16_pair(w.y); v[2] = bf16_pair(w.z); v[3] = bf16_pair(w.w);
     }
     __device__ __forceinline__ void set(const float2 (&v)[4]) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            w[i] = make_uint4(__float_as_uint(v[2 * i].x), __float_as_uint(v[2 * i].y), __float_as_uint(v[2 * i + 1].x),
-                              __float_as_uint(v[2 * i + 1].y));
+        w = make_uint4(to_bf16_pair(v[0]), to_bf16_pair(v[1]), to_bf16_pair(v[2]), to_bf16_pair(v[3]));
     }
-    __device__ __forceinline__ void load(const float* p, int) { w[0] = ld16(p); w[1] = ld16(p + 4); }
-    __device__ __forceinline__ void store(float* p, int) const { st16(p, w[0]); st16(p + 4, w[1]); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, int) { w = ld16(p); }
+    __device__ __forceinline__ void load_shared(uint32_t at) { w = lds16(at); }
+    __device__ __forceinline__ void store(__nv_bfloat16* p, int) const { st16(p, w); }
 };
 template <>
-struct Piece<__nv_bfloat16, 8> {
-    uint4 w[1];
-    __device__ __forceinline__ void zero() { w[0] = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float2 (&v)[4]) const {
-        v[0] = bf16_pair(w[0].x); v[1] = bf16_pair(w[0].y); v[2] = bf16_pair(w[0].z); v[3] = bf16_pair(w[0].w);
+struct Piece<float, 4> {
+    uint4 w;
+    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float2 (&v)[2]) const {
+        v[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+        v[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
     }
-    __device__ __forceinline__ void set(const float2 (&v)[4]) {
-        w[0] = make_uint4(to_bf16_pair(v[0]), to_bf16_pair(v[1]), to_bf16_pair(v[2]), to_bf16_pair(v[3]));
+    __device__ __forceinline__ void set(const float2 (&v)[2]) {
+        w = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
     }
-    __device__ __forceinline__ void load(const __nv_bfloat16* p, int) { w[0] = ld16(p); }
-    __device__ __forceinline__ void store(__nv_bfloat16* p, int) const { st16(p, w[0]); }
+    __device__ __forceinline__ void load(const float* p, int) { w = ld16(p); }
+    __device__ __forceinline__ void load_shared(uint32_t at) { w = lds16(at); }
+    __device__ __forceinline__ void store(float* p, int) const { st16(p, w); }
+};
+template <>
+struct Piece<__nv_bfloat16, 4> {
+    uint2 w;
+    __device__ __forceinline__ void zero() { w = make_uint2(0, 0); }
+    __device__ __forceinline__ void get(float2 (&v)[2]) const { v[0] = bf16_pair(w.x); v[1] = bf16_pair(w.y); }
+    __device__ __forceinline__ void set(const float2 (&v)[2]) { w = make_uint2(to_bf16_pair(v[0]), to_bf16_pair(v[1])); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, int) { w = ld8(p); }
+    __device__ __forceinline__ void load_shared(uint32_t at) { w = lds8(at); }
+    __device__ __forceinline__ void store(__nv_bfloat16* p, int) const {
+        asm volatile("st.global.v2.u32 [%0], {%1,%2};" ::"l"(p), "r"(w.x), "r"(w.y) : "memory");
+    }
 };
 // Two columns, the second of which may lie behind the row's end (left == 1).
 template <typename T>
@@ -128,8 +156,10 @@ struct Piece<T, 2> {
     }
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+template <int bytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+    if constexpr (bytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits for the oldest of the groups in flight (stages - 1 of them, or one).
@@ -139,46 +169,41 @@ __device__ __forceinline__ void cp_async_wait(int stages) {
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// 16-byte parts of 8 columns; a part of every thread lies side by side.
-template <typename T>
-constexpr int kParts = sizeof(T) / 2;
-template <typename T, int N>
-__device__ __forceinline__ uint32_t ring_bytes() { return (uint32_t)(N * kParts<T> * blockDim.x * 16); }
+// A piece of every thread lies side by side in a ring slot.
+template <typename T, int V>
+constexpr int kBytes = V * (int)sizeof(T);
+template <typename T, int V, int N>
+__device__ __forceinline__ uint32_t ring_bytes() { return (uint32_t)(N * blockDim.x * kBytes<T, V>); }
+template <typename T, int V>
+__device__ __forceinline__ uint32_t ring_place(uint32_t array, int i) {
+    return array + (i * blockDim.x + threadIdx.x) * kBytes<T, V>;
+}
 
-// Copies this thread's pieces of a row (row: its first column's address) to dst (its place in the slot).
-template <typename T, int N>
-__device__ __forceinline__ void ring_copy(uint32_t dst, const T* row, int H) {
+// Copies this thread's pieces of a row (row: its first column's address) to an array of a slot.
+template <typename T, int V, int N>
+__device__ __forceinline__ void ring_copy(uint32_t array, const T* row, int H) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        if ((int)(i * blockDim.x + threadIdx.x) * 8 < H)
-#pragma unroll
-            for (int j = 0; j < kParts<T>; ++j)
-                cp_async16(dst + (i * kParts<T> + j) * blockDim.x * 16,
-                           reinterpret_cast<const char*>(row + i * blockDim.x * 8) + 16 * j);
-}
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-    uint4 r;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
-    return r;
+        if ((int)(i * blockDim.x + threadIdx.x) * V < H)
+            cp_async<kBytes<T, V>>(ring_place<T, V>(array, i), row + i * blockDim.x * V);
 }
 // Zeroes this thread's places in the ring that no copy fills: columns behind
 // the row's end, and (all) an array that is absent. Reads then need no conditions.
-template <typename T, int N>
-__device__ __forceinline__ void ring_clear(uint32_t dst, bool all, int H) {
+template <typename T, int V, int N>
+__device__ __forceinline__ void ring_clear(uint32_t array, bool all, int H) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        if (all || (int)(i * blockDim.x + threadIdx.x) * 8 >= H)
-#pragma unroll
-            for (int j = 0; j < kParts<T>; ++j)
-                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + (i * kParts<T> + j) * blockDim.x * 16), "r"(0)
-                             : "memory");
+        if (all || (int)(i * blockDim.x + threadIdx.x) * V >= H) {
+            const uint32_t at = ring_place<T, V>(array, i);
+            if constexpr (kBytes<T, V> == 16) asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+            else asm volatile("st.shared.v2.u32 [%0], {%1,%1};" ::"r"(at), "r"(0) : "memory");
+        }
 }
 // This thread's piece i of a row: from its ring slot, or from memory (row: its first column's address).
 template <typename T, int V, bool ring>
-__device__ __forceinline__ void take(Piece<T, V>& r, bool on, int i, uint32_t slot, const T* row, int H) {
+__device__ __forceinline__ void take(Piece<T, V>& r, bool on, int i, uint32_t array, const T* row, int H) {
     if constexpr (ring) {
-#pragma unroll
-        for (int j = 0; j < kParts<T>; ++j) r.w[j] = lds16(slot + (i * kParts<T> + j) * blockDim.x * 16);
+        r.load_shared(ring_place<T, V>(array, i));
     } else {
         const int left = H - (int)(i * blockDim.x + threadIdx.x) * V;
         r.zero();
@@ -237,10 +262,10 @@ template <int V>
 __device__ __forceinline__ void load_columns(const float* g, int c, int H, float2 (&v)[V / 2]) {
 #pragma unroll
     for (int j = 0; j < V / 2; ++j) v[j] = both(c < H && !g ? 1.0f : 0.0f);
-    if constexpr (V == 8) {
+    if constexpr (V >= 4) {
         if (c >= H || !g) return;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < V / 4; ++j) {
             const float4 f = __ldg(reinterpret_cast<const float4*>(g + c) + j);
             v[2 * j] = make_float2(f.x, f.y);
             v[2 * j + 1] = make_float2(f.z, f.w);
@@ -294,34 +319,37 @@ __device__ __forceinline__ float row_scale(const Piece<T, V> (&r)[N], int H, flo
     return rms_scale(dd[0], H, eps);
 }
 
+// The launch bound of 80 registers lets two blocks of 384 threads share an SM,
+// one row's sums under the other's copies: 2048 x 6144 bf16 (101 MB) took 20 us,
+// with one block an SM 23.
+constexpr int kForwardThreads = 768;
+
 // `single`: one row a block, read straight into registers by twice the threads.
 // Such a launch is as long as its code, since it runs all of it once from cold
 // instruction caches: with the ring one row of 6144 took 6.3 us, without 4.4.
-// At 2048 x 6144 bf16 (x, y, x_out, n: 101 MB) the launch bound of 80 registers
-// lets two blocks of 384 threads share an SM, one row's sums under another's copies.
 template <typename XT, typename YT, typename NT, int V, int N, bool single>
-__global__ void __launch_bounds__(768) block_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kForwardThreads) block_norm_kernel(const NormArgs a) {
     __shared__ float red[2][32];
     __shared__ double red64[2][32];
     extern __shared__ __align__(16) unsigned char ring_mem[];
     const int H = a.H, stages = a.stages, c0 = threadIdx.x * V;
     const bool has_prev = a.has_prev, post = a.post_norm, has_next = a.has_next;
     const float inv = 1.0f / (float)H;
-    constexpr bool kRing = V == 8 && !single;
-    const uint32_t xb = kRing ? ring_bytes<XT, N>() : 0;
-    const uint32_t slot_bytes = kRing ? xb + ring_bytes<YT, N>() : 0;
-    const uint32_t ring = smem_addr(ring_mem) + threadIdx.x * 16;
+    constexpr bool kRing = V >= 4 && !single;
+    const uint32_t xb = kRing ? ring_bytes<XT, V, N>() : 0;
+    const uint32_t slot_bytes = kRing ? xb + ring_bytes<YT, V, N>() : 0;
+    const uint32_t ring = smem_addr(ring_mem);
     if constexpr (kRing)
         for (int i = 0; i < stages; ++i) {
-            ring_clear<XT, N>(ring + i * slot_bytes, false, H);
-            ring_clear<YT, N>(ring + i * slot_bytes + xb, !has_prev, H);
+            ring_clear<XT, V, N>(ring + i * slot_bytes, false, H);
+            ring_clear<YT, V, N>(ring + i * slot_bytes + xb, !has_prev, H);
         }
     int pt = blockIdx.x;  // the next row to copy
     auto prefetch = [&](int slot) {
         if constexpr (kRing) {
             if (pt < a.T) {
-                ring_copy<XT, N>(ring + slot * slot_bytes, (const XT*)a.x + (size_t)pt * a.ldx + c0, H);
-                if (has_prev) ring_copy<YT, N>(ring + slot * slot_bytes + xb, (const YT*)a.y + (size_t)pt * a.ldy + c0, H);
+                ring_copy<XT, V, N>(ring + slot * slot_bytes, (const XT*)a.x + (size_t)pt * a.ldx + c0, H);
+                if (has_prev) ring_copy<YT, V, N>(ring + slot * slot_bytes + xb, (const YT*)a.y + (size_t)pt * a.ldy + c0, H);
             }
             cp_async_commit();
             pt += gridDim.x;
@@ -510,32 +538,33 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
     __shared__ float red[2][16 * 8];
     __shared__ double red64[32 * 6];
     extern __shared__ __align__(16) unsigned char ring_mem[];
+    constexpr bool kRing = V >= 4;
     const int H = a.H, stages = a.stages, c0 = threadIdx.x * V;
     const bool has_prev = a.has_prev, has_next = a.has_next, has_o = a.dxo != nullptr, post = a.post_norm;
     uint32_t yo = 0, oo = 0, no = 0, slot_bytes = 0;  // offsets of y, dxo and dn in a slot
-    if constexpr (V == 8) {
-        yo = ring_bytes<XT, N>();
-        oo = yo + ring_bytes<YT, N>();
-        no = oo + ring_bytes<XT, N>();
-        slot_bytes = no + ring_bytes<NT, N>();
+    if constexpr (kRing) {
+        yo = ring_bytes<XT, V, N>();
+        oo = yo + ring_bytes<YT, V, N>();
+        no = oo + ring_bytes<XT, V, N>();
+        slot_bytes = no + ring_bytes<NT, V, N>();
     }
-    const uint32_t ring = smem_addr(ring_mem) + threadIdx.x * 16;
-    if constexpr (V == 8)
+    const uint32_t ring = smem_addr(ring_mem);
+    if constexpr (kRing)
         for (int i = 0; i < stages; ++i) {
-            ring_clear<XT, N>(ring + i * slot_bytes, false, H);
-            ring_clear<YT, N>(ring + i * slot_bytes + yo, !has_prev, H);
-            ring_clear<XT, N>(ring + i * slot_bytes + oo, !has_o, H);
-            ring_clear<NT, N>(ring + i * slot_bytes + no, !has_next, H);
+            ring_clear<XT, V, N>(ring + i * slot_bytes, false, H);
+            ring_clear<YT, V, N>(ring + i * slot_bytes + yo, !has_prev, H);
+            ring_clear<XT, V, N>(ring + i * slot_bytes + oo, !has_o, H);
+            ring_clear<NT, V, N>(ring + i * slot_bytes + no, !has_next, H);
         }
     int pt = blockIdx.x;  // the next row to copy
     auto prefetch = [&](int slot) {
-        if constexpr (V == 8) {
+        if constexpr (kRing) {
             if (pt < a.T) {
                 const uint32_t at = ring + slot * slot_bytes;
-                ring_copy<XT, N>(at, (const XT*)a.x + (size_t)pt * a.ldx + c0, H);
-                if (has_prev) ring_copy<YT, N>(at + yo, (const YT*)a.y + (size_t)pt * a.ldy + c0, H);
-                if (has_o) ring_copy<XT, N>(at + oo, (const XT*)a.dxo + (size_t)pt * a.lddxo + c0, H);
-                if (has_next) ring_copy<NT, N>(at + no, (const NT*)a.dn + (size_t)pt * a.lddn + c0, H);
+                ring_copy<XT, V, N>(at, (const XT*)a.x + (size_t)pt * a.ldx + c0, H);
+                if (has_prev) ring_copy<YT, V, N>(at + yo, (const YT*)a.y + (size_t)pt * a.ldy + c0, H);
+                if (has_o) ring_copy<XT, V, N>(at + oo, (const XT*)a.dxo + (size_t)pt * a.lddxo + c0, H);
+                if (has_next) ring_copy<NT, V, N>(at + no, (const NT*)a.dn + (size_t)pt * a.lddn + c0, H);
             }
             cp_async_commit();
             pt += gridDim.x;
@@ -559,7 +588,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
     for (int i = 1; i < stages - 1; ++i) prefetch(i);
     // V = 2: the next row's columns are loaded while a row is worked on, where the registers allow it
     constexpr bool kAhead = V == 2 && N <= 4;
-    constexpr int kKept = V == 8 ? 1 : N;
+    constexpr int kKept = kRing ? 1 : N;
     Piece<XT, V> rs[kKept], ro[kKept];
     Piece<YT, V> ry[kKept];
     Piece<NT, V> rn[kKept];
@@ -577,7 +606,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
     const float inv = 1.0f / (float)H;
     const bool tiny_s = has_next && a.eps_pre < 1e-12f, tiny_y = post && a.eps_post < 1e-12f;  // see sum_ok
     for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-        if constexpr (V == 8) {
+        if constexpr (kRing) {
             cp_async_wait(stages);
             // into the slot of the row before this one, which this thread has read
             if (stages > 1) prefetch(slot == 0 ? stages - 1 : slot - 1);
@@ -601,12 +630,12 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
             if constexpr (kAhead) {
                 s[0] = ks[i], y[0] = ky[i], o[0] = ko[i], n[0] = kn[i];
             } else {
-                const int k = V == 8 ? 0 : i;
-                if (V == 8 || pass == 0) {
-                    take<XT, V, V == 8>(rs[k], true, i, at, (const XT*)a.x + (size_t)t * a.ldx + c0, H);
-                    take<YT, V, V == 8>(ry[k], has_prev, i, at + yo, (const YT*)a.y + (size_t)t * a.ldy + c0, H);
-                    take<XT, V, V == 8>(ro[k], has_o, i, at + oo, (const XT*)a.dxo + (size_t)t * a.lddxo + c0, H);
-                    take<NT, V, V == 8>(rn[k], has_next, i, at + no, (const NT*)a.dn + (size_t)t * a.lddn + c0, H);
+                const int k = kRing ? 0 : i;
+                if (kRing || pass == 0) {
+                    take<XT, V, kRing>(rs[k], true, i, at, (const XT*)a.x + (size_t)t * a.ldx + c0, H);
+                    take<YT, V, kRing>(ry[k], has_prev, i, at + yo, (const YT*)a.y + (size_t)t * a.ldy + c0, H);
+                    take<XT, V, kRing>(ro[k], has_o, i, at + oo, (const XT*)a.dxo + (size_t)t * a.lddxo + c0, H);
+                    take<NT, V, kRing>(rn[k], has_next, i, at + no, (const NT*)a.dn + (size_t)t * a.lddn + c0, H);
                 }
                 rs[k].get(s);
                 ry[k].get(y);
@@ -721,7 +750,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
         for (int i = 0; i < N; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * V;
             float* out = a.part + (size_t)blockIdx.x * 2 * H + c;
-            if constexpr (V == 8) {
+            if constexpr (kRing) {
                 if (c >= H) continue;
 #pragma unroll
                 for (int j = 0; j < P; j += 2) {
@@ -866,34 +895,33 @@ __global__ void __launch_bounds__(512) sum_parts_kernel(const NormArgs a, int n,
     if (dgate) dgate[c] = acc * (a.post ? a.post[c] : 1.0f);
 }
 
+constexpr int kSms = 148;
+constexpr int kSingleRows = kSms;  // up to here a block takes one row without the ring
 // V, N and threads for rows of H columns, up to 512 threads; N == 0: too wide
-// for registers.
+// for registers. V: columns that all rows take at a time (8 or 4), or 2.
 struct Shape {
     int V, N, threads;
 };
-Shape shape_of(int H, bool vec) {
-    const int V = vec ? 8 : 2;
+Shape shape_of(int H, int V) {
     const int n = (H + V - 1) / V;
     for (int N : {1, 2, 4, 8}) {
-        if (vec && N > 2) break;
+        if (N * V > 16) break;
         const int th = ((n + N - 1) / N + 31) / 32 * 32;
         if (th <= 512) return {V, N, th};
     }
     return {V, 0, 512};
 }
 
-constexpr int kSms = 148;
-constexpr int kSingleRows = kSms;  // up to here a block takes one row without the ring
 // Blocks that share an SM: as many as their registers let (80 a thread
 // forward, 128 backward), at most 8.
 int blocks_per_sm(int threads, bool fwd) {
-    const int n = (fwd ? 768 : 512) / threads;
+    const int n = (fwd ? kForwardThreads : 512) / threads;
     return n < 1 ? 1 : n > 8 ? 8 : n;
 }
 // Blocks of a persistent launch over T rows. The workspace's size depends on
 // it: it must not depend on the alignment of a call's rows.
 int grid_of(int T, int H, bool fwd) {
-    const int g = kSms * blocks_per_sm(shape_of(H, H % 8 == 0).threads, fwd);
+    const int g = kSms * blocks_per_sm(shape_of(H, H % 8 == 0 ? 8 : H % 4 == 0 ? 4 : 2).threads, fwd);
     return T < g ? T : g;
 }
 // Ring slots of `row` bytes (at most 128 KB) that fit beside the other blocks of an SM.
@@ -906,7 +934,7 @@ using B = __nv_bfloat16;
 using Kernel = void (*)(NormArgs);
 
 cudaError_t launch_rows(Kernel k, NormArgs& a, const Shape& s, size_t col_bytes, int grid, bool fwd, cudaStream_t st) {
-    const size_t row = s.V == 8 && s.N ? col_bytes * 8 * s.N * s.threads : 0;
+    const size_t row = s.V >= 4 && s.N ? col_bytes * s.V * s.N * s.threads : 0;
     a.stages = row ? stages_of(row, s.threads, (a.T + grid - 1) / grid, fwd) : 0;
     const size_t smem = a.stages * row;
     if (smem > 40 * 1024) {
@@ -917,45 +945,74 @@ cudaError_t launch_rows(Kernel k, NormArgs& a, const Shape& s, size_t col_bytes,
 }
 
 template <typename XT, typename YT, typename NT>
-cudaError_t forward_typed(NormArgs& a, bool vec, cudaStream_t st) {
-    if (vec && a.T <= kSingleRows && a.H <= 8 * 768)
-        return launch(block_norm_kernel<XT, YT, NT, 8, 1, true>, a.T, (a.H / 8 + 31) / 32 * 32, 0, st, false, a);
-    const Shape s = shape_of(a.H, vec);
-    const Kernel k = s.N == 0   ? block_norm_wide_kernel<XT, YT, NT>
-                     : s.V == 8 ? (s.N == 1 ? block_norm_kernel<XT, YT, NT, 8, 1, false> : block_norm_kernel<XT, YT, NT, 8, 2, false>)
-                     : s.N == 1 ? block_norm_kernel<XT, YT, NT, 2, 1, false>
-                     : s.N == 2 ? block_norm_kernel<XT, YT, NT, 2, 2, false>
-                     : s.N == 4 ? block_norm_kernel<XT, YT, NT, 2, 4, false>
-                                : block_norm_kernel<XT, YT, NT, 2, 8, false>;
+cudaError_t forward_typed(NormArgs& a, int V, cudaStream_t st) {
+    constexpr bool narrow = sizeof(XT) + sizeof(YT) + sizeof(NT) == 6;  // all bf16
+    const int n = (a.H + V - 1) / V;
+    if (a.T <= kSingleRows && V >= 4 && n <= kForwardThreads * (8 / V)) {
+        const int N = 8 / V, th = ((n + N - 1) / N + 31) / 32 * 32;
+        if constexpr (narrow)
+            if (V == 8) return launch(block_norm_kernel<XT, YT, NT, 8, 1, true>, a.T, th, 0, st, false, a);
+        return launch(block_norm_kernel<XT, YT, NT, 4, 2, true>, a.T, th, 0, st, false, a);
+    }
+    const Shape s = shape_of(a.H, V);
+    Kernel k = block_norm_wide_kernel<XT, YT, NT>;
+    if (s.N && V == 8) {
+        if constexpr (narrow) k = s.N == 1 ? block_norm_kernel<XT, YT, NT, 8, 1, false> : block_norm_kernel<XT, YT, NT, 8, 2, false>;
+    } else if (s.N && V == 4) {
+        k = s.N == 1   ? block_norm_kernel<XT, YT, NT, 4, 1, false>
+            : s.N == 2 ? block_norm_kernel<XT, YT, NT, 4, 2, false>
+                       : block_norm_kernel<XT, YT, NT, 4, 4, false>;
+    } else if (s.N) {
+        k = s.N == 1   ? block_norm_kernel<XT, YT, NT, 2, 1, false>
+            : s.N == 2 ? block_norm_kernel<XT, YT, NT, 2, 2, false>
+            : s.N == 4 ? block_norm_kernel<XT, YT, NT, 2, 4, false>
+                       : block_norm_kernel<XT, YT, NT, 2, 8, false>;
+    }
     return launch_rows(k, a, s, sizeof(XT) + sizeof(YT), s.N ? grid_of(a.T, a.H, true) : a.T, true, st);
 }
 
 template <typename XT, typename YT, typename NT>
-cudaError_t backward_typed(NormArgs& a, bool vec, cudaStream_t st) {
-    const Shape s = shape_of(a.H, vec);
-    const Kernel k = s.N == 0 ? block_norm_backward_wide_kernel<XT, YT, NT>
-                     : s.V == 8
-                         ? (s.N == 1 ? block_norm_backward_kernel<XT, YT, NT, 8, 1> : block_norm_backward_kernel<XT, YT, NT, 8, 2>)
-                     : s.N == 1 ? block_norm_backward_kernel<XT, YT, NT, 2, 1>
-                     : s.N == 2 ? block_norm_backward_kernel<XT, YT, NT, 2, 2>
-                     : s.N == 4 ? block_norm_backward_kernel<XT, YT, NT, 2, 4>
-                                : block_norm_backward_kernel<XT, YT, NT, 2, 8>;
-    const size_t col = 2 * sizeof(XT) + sizeof(YT) + sizeof(NT);
-    return launch_rows(k, a, s, col, grid_of(a.T, a.H, false), false, st);
+cudaError_t backward_typed(NormArgs& a, int V, cudaStream_t st) {
+    constexpr bool narrow = sizeof(XT) + sizeof(YT) + sizeof(NT) == 6;
+    const Shape s = shape_of(a.H, V);
+    Kernel k = block_norm_backward_wide_kernel<XT, YT, NT>;
+    if (s.N && V == 8) {
+        if constexpr (narrow) k = s.N == 1 ? block_norm_backward_kernel<XT, YT, NT, 8, 1> : block_norm_backward_kernel<XT, YT, NT, 8, 2>;
+    } else if (s.N && V == 4) {
+        k = s.N == 1   ? block_norm_backward_kernel<XT, YT, NT, 4, 1>
+            : s.N == 2 ? block_norm_backward_kernel<XT, YT, NT, 4, 2>
+                       : block_norm_backward_kernel<XT, YT, NT, 4, 4>;
+    } else if (s.N) {
+        k = s.N == 1   ? block_norm_backward_kernel<XT, YT, NT, 2, 1>
+            : s.N == 2 ? block_norm_backward_kernel<XT, YT, NT, 2, 2>
+            : s.N == 4 ? block_norm_backward_kernel<XT, YT, NT, 2, 4>
+                       : block_norm_backward_kernel<XT, YT, NT, 2, 8>;
+    }
+    return launch_rows(k, a, s, 2 * sizeof(XT) + sizeof(YT) + sizeof(NT), grid_of(a.T, a.H, false), false, st);
 }
 
 template <bool fwd>
-cudaError_t by_type(NormArgs& a, coli_dtype xt, coli_dtype yt, coli_dtype nt, bool vec, cudaStream_t st) {
+cudaError_t by_type(NormArgs& a, coli_dtype xt, coli_dtype yt, coli_dtype nt, int V, cudaStream_t st) {
     auto go = [&](auto x, auto y, auto n) {
-        if constexpr (fwd) return forward_typed<decltype(x), decltype(y), decltype(n)>(a, vec, st);
-        else return backward_typed<decltype(x), decltype(y), decltype(n)>(a, vec, st);
+        if constexpr (fwd) return forward_typed<decltype(x), decltype(y), decltype(n)>(a, V, st);
+        else return backward_typed<decltype(x), decltype(y), decltype(n)>(a, V, st);
     };
     auto with_n = [&](auto x, auto y) { return nt == COLI_F32 ? go(x, y, float()) : go(x, y, B()); };
     auto with_y = [&](auto x) { return yt == COLI_F32 ? with_n(x, float()) : with_n(x, B()); };
     return xt == COLI_F32 ? with_y(float()) : with_y(B());
 }
 
-bool gain_vec(const float* p) { return ((uintptr_t)p & 15u) == 0; }
+// Columns that all of a call's rows and arrays take at a time: 8 (all bf16), 4,
+// or 2 read one by one. m: the matrices, NULL where absent.
+int columns_of(const NormArgs& a, std::initializer_list<const Mat*> m) {
+    if (((uintptr_t)a.pre | (uintptr_t)a.post | (uintptr_t)a.gate) & 15u) return 2;
+    for (int V : {8, 4}) {
+        bool ok = true;
+        for (const Mat* x : m) ok = ok && (!x || (x->takes(V) && (V == 4 || x->t == COLI_BF16)));
+        if (ok) return V;
+    }
+    return 2;
+}
 
 #define REQUIRE(cond, msg)                                \
     do {                                                  \
@@ -1024,20 +1081,18 @@ coli_status block_norm_launch(const coli_block_params* prev, const coli_block_pa
     a.x = x->p;
     a.ldx = x->stride;
     a.token = token_gate;
-    bool vec = H % 8 == 0 && x->vec() && gain_vec(a.pre) && gain_vec(a.post) && gain_vec(a.gate);
     if (prev) {
         a.y = y->p;
         a.ldy = y->stride;
         a.xo = x_out->p ? const_cast<void*>(x_out->p) : nullptr;
         a.ldxo = x_out->stride;
-        vec = vec && y->vec() && x_out->vec();
     }
     if (next) {
         a.n = const_cast<void*>(n->p);
         a.ldn = n->stride;
-        vec = vec && n->vec();
     }
-    const cudaError_t e = by_type<true>(a, x->t, prev ? y->t : x->t, next ? n->t : x->t, vec, st);
+    const int V = columns_of(a, {x, prev ? y : nullptr, prev ? x_out : nullptr, next ? n : nullptr});
+    const cudaError_t e = by_type<true>(a, x->t, prev ? y->t : x->t, next ? n->t : x->t, V, st);
     return e == cudaSuccess ? COLI_OK : block_cuda_fail(e, "block norm");
 }
 
@@ -1176,9 +1231,8 @@ COLI_API coli_status coli_block_norm_backward(const coli_block_params* prev, con
     a.part = want ? (float*)work : nullptr;
     cudaError_t e = cudaSuccess;
     if (T > 0) {
-        const bool vec = H % 8 == 0 && ms.vec() && (!prev || my.vec()) && (!next || mn.vec()) && (!dx_out || mo.vec()) &&
-                         (!dx || mdx.vec()) && (!dy || mdy.vec()) && gain_vec(a.pre) && gain_vec(a.post) && gain_vec(a.gate);
-        e = by_type<false>(a, x_dtype, prev ? y_dtype : x_dtype, next ? n_dtype : x_dtype, vec, s);
+        const int V = columns_of(a, {&ms, in[1], in[2], in[3], dx ? &mdx : nullptr, dy ? &mdy : nullptr});
+        e = by_type<false>(a, x_dtype, prev ? y_dtype : x_dtype, next ? n_dtype : x_dtype, V, s);
         if (e != cudaSuccess) return block_cuda_fail(e, "block norm backward");
     }
     if (!want) return COLI_OK;

@@ -144,12 +144,13 @@ size_t rank_smem(int E) { return sizeof(int32_t) * ((size_t)kRankWarps * E + 32)
 // ---------------------------------------------------------------------------
 // The same sort in one launch for up to kClusterSlots slots: a cluster of eight
 // blocks, a chunk each, which read each other's counts from shared memory. A
-// warp's first 64 slots stay in registers between the two passes. 16384 slots
-// of 256 experts took the two launches above 10 us, this one 5 (and the rows
-// kernel starts meanwhile).
+// warp's first 64 slots stay in registers between the two passes. With the rows
+// (256 columns of bf16), dispatch took 11.8 us for 24000 slots where the two
+// launches above took 12.8, but 15.5 against 13.6 for 32768: eight blocks are
+// then too few.
 // ---------------------------------------------------------------------------
 constexpr int kCluster = 8;
-constexpr int kClusterSlots = 1 << 17;
+constexpr int kClusterSlots = 24576;
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -244,69 +245,92 @@ __global__ void __launch_bounds__(kRankThreads, 1) dispatch_sort_kernel(const in
     cluster_wait();
 }
 
-// rows[pos[t][k]] = x[t]: a thread reads V columns of a token once and writes
+// Pieces of V columns that a thread takes, a block's width apart: narrow pieces
+// would spend more loads on the positions than on the rows.
+template <int V>
+constexpr int kPieces = V >= 4 ? 1 : V == 2 ? 2 : 4;
+
+// rows[pos[t][k]] = x[t]: a thread reads its columns of a token once and writes
 // them K times. Bound by the K rows a token writes.
 template <typename XT, typename RT, int V>
 __global__ void __launch_bounds__(256) dispatch_rows_kernel(const XT* x, int64_t ldx, const int32_t* pos, int K, int H,
                                                             RT* rows, int64_t ldr) {
-    const int t = blockIdx.x;
-    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
-    Raw<XT, V> in;
-    float v[V];
-    if (c < H) {
-        in.load(x + (size_t)t * ldx + c);  // x is older than the sort: read while that still runs
+    constexpr int N = kPieces<V>;
+    const int t = blockIdx.x, step = blockDim.x * V;
+    const int c0 = blockIdx.y * N * step + threadIdx.x * V;
+    Raw<RT, V> out[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        Raw<XT, V> in;
+        in.zero();
+        if (c0 + i * step < H) in.load(x + (size_t)t * ldx + c0 + i * step);  // x is older than the sort: read while that still runs
+        float v[V];
         in.get(v);
+        out[i].set(v);
     }
     grid_wait();
-    if (c >= H) return;
-    Raw<RT, V> out;
-    out.set(v);
     for (int k = 0; k < K; ++k) {
         const int q = pos[(size_t)t * K + k];
-        if (q >= 0) out.store(rows + (size_t)q * ldr + c);
+        if (q < 0) continue;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (c0 + i * step < H) out[i].store(rows + (size_t)q * ldr + c0 + i * step);
     }
 }
 
-// y[t] = base[t] + sum_k w[t][k] rows[pos[t][k]], one thread per token and V
-// columns, the rows of eight slots in flight at a time. Bound by the K rows a
-// token reads.
+// y[t] = base[t] + sum_k w[t][k] rows[pos[t][k]], the rows of eight slots in
+// flight at a time. Bound by the K rows a token reads.
 template <typename RT, typename YT, int V>
-__global__ void __launch_bounds__(256) gather_sum_kernel(const int32_t* pos, const float* w, int K, const RT* rows,
-                                                         int64_t ldr, int64_t n_rows, int H, const YT* base,
-                                                         int64_t ldb, YT* y, int64_t ldy) {
+__global__ void __launch_bounds__(256, sizeof(RT) == 4 ? 4 : 3) gather_sum_kernel(const int32_t* pos, const float* w, int K, const RT* rows,
+                                                         int64_t ldr, int n_rows, int H, const YT* base, int64_t ldb,
+                                                         YT* y, int64_t ldy) {
     grid_wait();
-    const int t = blockIdx.x;
-    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
-    if (c >= H) return;
-    float acc[V];
-    Raw<YT, V> b;
-    b.zero();
-    if (base) b.load(base + (size_t)t * ldb + c);
-    b.get(acc);
+    constexpr int N = kPieces<V>;
+    const int t = blockIdx.x, step = blockDim.x * V;
+    const int c0 = blockIdx.y * N * step + threadIdx.x * V;
+    if (c0 >= H) return;
+    float acc[N][V];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        Raw<YT, V> b;
+        b.zero();
+        if (base && c0 + i * step < H) b.load(base + (size_t)t * ldb + c0 + i * step);
+        b.get(acc[i]);
+    }
     for (int k0 = 0; k0 < K; k0 += 8) {
-        Raw<RT, V> r[8];
         float wk[8];
-        bool on[8];
+        int q[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int k = k0 + j;
-            const int q = k < K ? pos[(size_t)t * K + k] : -1;
-            on[j] = q >= 0 && q < n_rows;
-            wk[j] = on[j] && w ? w[(size_t)t * K + k] : 1.0f;
-            if (on[j]) r[j].load(rows + (size_t)q * ldr + c);
+            q[j] = k < K ? pos[(size_t)t * K + k] : -1;
+            if (q[j] >= n_rows) q[j] = -1;
+            wk[j] = q[j] >= 0 && w ? w[(size_t)t * K + k] : 1.0f;
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (!on[j]) continue;
-            float v[V];
-            r[j].get(v);
+        for (int i = 0; i < N; ++i) {
+            const int c = c0 + i * step;
+            if (N > 1 && c >= H) break;
+            Raw<RT, V> r[8];
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = fmaf(wk[j], v[i], acc[i]);
+            for (int j = 0; j < 8; ++j)
+                if (q[j] >= 0) r[j].load(rows + (size_t)q[j] * ldr + c);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (q[j] < 0) continue;
+                float v[V];
+                r[j].get(v);
+#pragma unroll
+                for (int l = 0; l < V; ++l) acc[i][l] = fmaf(wk[j], v[l], acc[i][l]);
+            }
         }
     }
-    Raw<YT, V> out;
-    out.set(acc);
-    out.store(y + (size_t)t * ldy + c);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        Raw<YT, V> out;
+        out.set(acc[i]);
+        if (c0 + i * step < H) out.store(y + (size_t)t * ldy + c0 + i * step);
+    }
 }
 
 // drows[pos] = w dy[t], dweights = dot(dy[t], rows[pos]): one block per token,
@@ -374,23 +398,29 @@ int threads_for(int H, int V) {
     return n < 256 ? n : 256;
 }
 dim3 grid_for(int T, int H, int V, int threads) {
-    return dim3((unsigned)T, (unsigned)((H + V * threads - 1) / (V * threads)));
+    const int tile = V * threads * (V >= 4 ? 1 : V == 2 ? 2 : 4);  // kPieces
+    return dim3((unsigned)T, (unsigned)((H + tile - 1) / tile));
 }
 
-// The largest of 8, 4, 2 and 1 columns a thread that all these rows take.
+// The largest of 8, 4, 2 and 1 columns a thread that all these rows take; 8
+// only of bf16 (of fp32, a warp's two accesses would lie 32 bytes apart and
+// read every 32-byte sector twice).
 int columns_of(const Mat& a, const Mat& b, const Mat* c = nullptr) {
-    for (int V : {8, 4, 2})
+    for (int V : {8, 4, 2}) {
+        if (V == 8 && (a.t != COLI_BF16 || b.t != COLI_BF16)) continue;
         if (a.takes(V) && b.takes(V) && (!c || c->takes(V))) return V;
+    }
     return 1;
 }
 
 template <typename XT, typename RT>
 cudaError_t dispatch_rows(const Mat& x, const int32_t* pos, int T, int K, const Mat& rows, cudaStream_t st) {
     const int V = columns_of(x, rows), th = threads_for(x.cols, V);
-    auto k = V == 8   ? dispatch_rows_kernel<XT, RT, 8>
-             : V == 4 ? dispatch_rows_kernel<XT, RT, 4>
+    auto k = V == 4   ? dispatch_rows_kernel<XT, RT, 4>
              : V == 2 ? dispatch_rows_kernel<XT, RT, 2>
                       : dispatch_rows_kernel<XT, RT, 1>;
+    if constexpr (sizeof(XT) + sizeof(RT) == 4)
+        if (V == 8) k = dispatch_rows_kernel<XT, RT, 8>;
     return launch(k, grid_for(T, x.cols, V, th), th, 0, st, true, (const XT*)x.p, x.stride, pos, K, x.cols, (RT*)rows.p,
                   rows.stride);
 }
@@ -399,22 +429,24 @@ template <typename RT, typename YT>
 cudaError_t gather_sum(const int32_t* pos, const float* w, int T, int K, const Mat& rows, const Mat* base, const Mat& y,
                        cudaStream_t st, bool dependent) {
     const int V = columns_of(rows, y, base), th = threads_for(y.cols, V);
-    auto k = V == 8   ? gather_sum_kernel<RT, YT, 8>
-             : V == 4 ? gather_sum_kernel<RT, YT, 4>
+    auto k = V == 4   ? gather_sum_kernel<RT, YT, 4>
              : V == 2 ? gather_sum_kernel<RT, YT, 2>
                       : gather_sum_kernel<RT, YT, 1>;
-    return launch(k, grid_for(T, y.cols, V, th), th, 0, st, dependent, pos, w, K, (const RT*)rows.p, rows.stride, rows.rows,
-                  y.cols, (const YT*)(base ? base->p : nullptr), base ? base->stride : 0, (YT*)y.p, y.stride);
+    if constexpr (sizeof(RT) + sizeof(YT) == 4)
+        if (V == 8) k = gather_sum_kernel<RT, YT, 8>;
+    return launch(k, grid_for(T, y.cols, V, th), th, 0, st, dependent, pos, w, K, (const RT*)rows.p, rows.stride,
+                  (int)(rows.rows < INT32_MAX ? rows.rows : INT32_MAX), y.cols, (const YT*)(base ? base->p : nullptr), base ? base->stride : 0, (YT*)y.p, y.stride);
 }
 
 template <typename RT, typename YT>
 cudaError_t combine_backward(const int32_t* pos, const float* w, int T, int K, const Mat& dy, const Mat& rows,
                              const Mat* drows, float* dw, cudaStream_t st) {
     const int V = dw ? columns_of(dy, rows, drows) : columns_of(dy, *drows);
-    auto k = V == 8   ? combine_backward_kernel<RT, YT, 8>
-             : V == 4 ? combine_backward_kernel<RT, YT, 4>
+    auto k = V == 4   ? combine_backward_kernel<RT, YT, 4>
              : V == 2 ? combine_backward_kernel<RT, YT, 2>
                       : combine_backward_kernel<RT, YT, 1>;
+    if constexpr (sizeof(RT) + sizeof(YT) == 4)
+        if (V == 8) k = combine_backward_kernel<RT, YT, 8>;
     return launch(k, T, threads_for(dy.cols, V), 0, st, false, pos, w, K, (const YT*)dy.p, dy.stride, dy.cols,
                   (const RT*)rows.p, rows.stride, rows.rows, (RT*)(drows ? drows->p : nullptr), drows ? drows->stride : 0, dw);
 }
@@ -526,11 +558,12 @@ __global__ void __launch_bounds__(kFewThreads) dispatch_few_kernel(const Few a, 
 
 template <typename XT, typename RT>
 cudaError_t dispatch_few(const Few& a, const Mat& x, const Mat& rows, cudaStream_t st) {
-    const int V = a.move ? columns_of(x, rows) : 8;
-    auto k = V == 8   ? dispatch_few_kernel<XT, RT, 8>
-             : V == 4 ? dispatch_few_kernel<XT, RT, 4>
+    const int V = a.move ? columns_of(x, rows) : 4;
+    auto k = V == 4   ? dispatch_few_kernel<XT, RT, 4>
              : V == 2 ? dispatch_few_kernel<XT, RT, 2>
                       : dispatch_few_kernel<XT, RT, 1>;
+    if constexpr (sizeof(XT) + sizeof(RT) == 4)
+        if (V == 8) k = dispatch_few_kernel<XT, RT, 8>;
     const int tiles = a.move ? (a.H + V * kFewThreads - 1) / (V * kFewThreads) : 1;
     return launch(k, dim3(a.T + 1, tiles), kFewThreads, 0, st, false, a, (const XT*)x.p, (RT*)rows.p);
 }
