@@ -180,7 +180,8 @@ int64_t width_of(const at::Tensor& t, const char* name) {
     return sized(t.size(1), name);
 }
 
-// Runs f (which makes one library call through `call`) and returns its status to Python.
+// Runs f (which makes one library call through `call`) and returns its status
+// to Python. Nothing within `call` may throw: the interpreter's lock is released there.
 template <typename F>
 PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F f) {
     try {
@@ -207,17 +208,17 @@ coli_status call(F f) {
 ENTRY(dispatch) {
     return guarded(n, 10, [&] {
         const Slots s = slots_of(a[0], "ids");
-        const int64_t E = integer(a[2], "n_experts");
+        const int E = sized(integer(a[2], "n_experts"), "n_experts");
         const at::Tensor* x = tensor(a[1], "x");
         const int64_t H = x ? width_of(*x, "x") : 1;
         const Mat mx = mat(a[1], "x", s.T, H, s.dev), mr = mat(a[7], "rows", -1, H, s.dev);
         const Work w = work_of(a[8], s.dev);
         const int32_t* ids = ints(a[0], "ids", s.dev, s.T, s.K);
-        int32_t *counts = ints(a[3], "counts", s.dev, E), *offsets = ints(a[4], "offsets", s.dev, E + 1);
+        int32_t *counts = ints(a[3], "counts", s.dev, E), *offsets = ints(a[4], "offsets", s.dev, (int64_t)E + 1);
         int32_t *pos = ints(a[5], "pos", s.dev, s.T, s.K), *slot = ints(a[6], "slot", s.dev, (int64_t)s.T * s.K);
         const coli_stream st = stream_of(a[9], s.dev);
         return call([&] {
-            return coli_moe_dispatch(ids, s.T, s.K, sized(E, "n_experts"), mx.p, mx.t, mx.stride, (int)H, counts, offsets,
+            return coli_moe_dispatch(ids, s.T, s.K, E, mx.p, mx.t, mx.stride, (int)H, counts, offsets,
                                      pos, slot, mr.p, mr.t, mr.stride, mr.rows, w.p, w.bytes, s.dev, st);
         });
     });

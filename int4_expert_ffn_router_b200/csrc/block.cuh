@@ -16,6 +16,7 @@ struct DeviceGuard {
     explicit DeviceGuard(int dev) {
         if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
         if (prev != dev) ok = cudaSetDevice(dev) == cudaSuccess;
+        if (!ok) cudaGetLastError();  // reported by the caller, not left behind
     }
     ~DeviceGuard() {
         int cur = -1;
@@ -274,9 +275,10 @@ __device__ __forceinline__ void block_sum(F (&v)[NR], F* red) {
 }
 
 // dispatch.cu: y[t] = base[t] + sum_k w[t][k] rows[pos[t][k]] over the positions in
-// [0, rows.rows) (w NULL: 1). y, base: [T][H] of one type; dependent: see launch().
-cudaError_t launch_gather_sum(const int32_t* pos, const float* w, int T, int K, const Mat& rows, const Mat* base,
-                              const Mat& y, cudaStream_t st, bool dependent);
+// [0, rows.rows) (w NULL: 1; skip_zero: a slot of weight 0 is left out, whatever
+// its row holds). y, base: [T][H] of one type; dependent: see launch().
+cudaError_t launch_gather_sum(const int32_t* pos, const float* w, bool skip_zero, int T, int K, const Mat& rows,
+                              const Mat* base, const Mat& y, cudaStream_t st, bool dependent);
 
 // block_norm.cu: the norms around a block (coli_block_norm), arguments checked by the caller.
 coli_status block_norm_launch(const coli_block_params* prev, const coli_block_params* next, const Mat* x, const Mat* y,

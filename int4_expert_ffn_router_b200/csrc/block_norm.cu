@@ -913,10 +913,10 @@ Shape shape_of(int H, int V) {
 }
 
 // Blocks that share an SM: as many as their registers let (80 a thread
-// forward, 128 backward), at most 8.
+// forward, 128 backward), at most 16 (8: each block leaves its sums).
 int blocks_per_sm(int threads, bool fwd) {
-    const int n = (fwd ? kForwardThreads : 512) / threads;
-    return n < 1 ? 1 : n > 8 ? 8 : n;
+    const int n = (fwd ? kForwardThreads : 512) / threads, most = fwd ? 16 : 8;
+    return n < 1 ? 1 : n > most ? most : n;
 }
 // Blocks of a persistent launch over T rows. The workspace's size depends on
 // it: it must not depend on the alignment of a call's rows.

@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(256) dispatch_rows_kernel(const XT* x, int64_t
 // y[t] = base[t] + sum_k w[t][k] rows[pos[t][k]], the rows of eight slots in
 // flight at a time. Bound by the K rows a token reads.
 template <typename RT, typename YT, int V>
-__global__ void __launch_bounds__(256, sizeof(RT) == 4 ? 4 : 3) gather_sum_kernel(const int32_t* pos, const float* w, int K, const RT* rows,
+__global__ void __launch_bounds__(256, sizeof(RT) == 4 ? 4 : 3) gather_sum_kernel(const int32_t* pos, const float* w, bool skip_zero, int K, const RT* rows,
                                                          int64_t ldr, int n_rows, int H, const YT* base, int64_t ldb,
                                                          YT* y, int64_t ldy) {
     grid_wait();
@@ -306,6 +306,7 @@ __global__ void __launch_bounds__(256, sizeof(RT) == 4 ? 4 : 3) gather_sum_kerne
             q[j] = k < K ? pos[(size_t)t * K + k] : -1;
             if (q[j] >= n_rows) q[j] = -1;
             wk[j] = q[j] >= 0 && w ? w[(size_t)t * K + k] : 1.0f;
+            if (skip_zero && wk[j] == 0.0f) q[j] = -1;
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -393,13 +394,14 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const int32_t* po
     }
 }
 
-int threads_for(int H, int V) {
-    const int n = ((H + V - 1) / V + 31) / 32 * 32;
-    return n < 256 ? n : 256;
-}
-dim3 grid_for(int T, int H, int V, int threads) {
-    const int tile = V * threads * (V >= 4 ? 1 : V == 2 ? 2 : 4);  // kPieces
-    return dim3((unsigned)T, (unsigned)((H + tile - 1) / tile));
+// Threads of a block, and blocks of `pieces` pieces a thread, for rows of H
+// columns: blocks of up to 256 threads that share the columns evenly.
+struct Tiles {
+    int threads, n;
+};
+Tiles tiles_of(int H, int V, int pieces = 1) {
+    const int all = (H + V * pieces - 1) / (V * pieces), n = (all + 255) / 256;
+    return {((all + n - 1) / n + 31) / 32 * 32, n};
 }
 
 // The largest of 8, 4, 2 and 1 columns a thread that all these rows take; 8
@@ -415,26 +417,28 @@ int columns_of(const Mat& a, const Mat& b, const Mat* c = nullptr) {
 
 template <typename XT, typename RT>
 cudaError_t dispatch_rows(const Mat& x, const int32_t* pos, int T, int K, const Mat& rows, cudaStream_t st) {
-    const int V = columns_of(x, rows), th = threads_for(x.cols, V);
+    const int V = columns_of(x, rows);
+    const Tiles g = tiles_of(x.cols, V, V >= 4 ? 1 : V == 2 ? 2 : 4);  // kPieces
     auto k = V == 4   ? dispatch_rows_kernel<XT, RT, 4>
              : V == 2 ? dispatch_rows_kernel<XT, RT, 2>
                       : dispatch_rows_kernel<XT, RT, 1>;
     if constexpr (sizeof(XT) + sizeof(RT) == 4)
         if (V == 8) k = dispatch_rows_kernel<XT, RT, 8>;
-    return launch(k, grid_for(T, x.cols, V, th), th, 0, st, true, (const XT*)x.p, x.stride, pos, K, x.cols, (RT*)rows.p,
+    return launch(k, dim3(T, g.n), g.threads, 0, st, true, (const XT*)x.p, x.stride, pos, K, x.cols, (RT*)rows.p,
                   rows.stride);
 }
 
 template <typename RT, typename YT>
-cudaError_t gather_sum(const int32_t* pos, const float* w, int T, int K, const Mat& rows, const Mat* base, const Mat& y,
-                       cudaStream_t st, bool dependent) {
-    const int V = columns_of(rows, y, base), th = threads_for(y.cols, V);
+cudaError_t gather_sum(const int32_t* pos, const float* w, bool skip_zero, int T, int K, const Mat& rows, const Mat* base,
+                       const Mat& y, cudaStream_t st, bool dependent) {
+    const int V = columns_of(rows, y, base);
+    const Tiles g = tiles_of(y.cols, V, V >= 4 ? 1 : V == 2 ? 2 : 4);  // kPieces
     auto k = V == 4   ? gather_sum_kernel<RT, YT, 4>
              : V == 2 ? gather_sum_kernel<RT, YT, 2>
                       : gather_sum_kernel<RT, YT, 1>;
     if constexpr (sizeof(RT) + sizeof(YT) == 4)
         if (V == 8) k = gather_sum_kernel<RT, YT, 8>;
-    return launch(k, grid_for(T, y.cols, V, th), th, 0, st, dependent, pos, w, K, (const RT*)rows.p, rows.stride,
+    return launch(k, dim3(T, g.n), g.threads, 0, st, dependent, pos, w, skip_zero, K, (const RT*)rows.p, rows.stride,
                   (int)(rows.rows < INT32_MAX ? rows.rows : INT32_MAX), y.cols, (const YT*)(base ? base->p : nullptr), base ? base->stride : 0, (YT*)y.p, y.stride);
 }
 
@@ -447,7 +451,8 @@ cudaError_t combine_backward(const int32_t* pos, const float* w, int T, int K, c
                       : combine_backward_kernel<RT, YT, 1>;
     if constexpr (sizeof(RT) + sizeof(YT) == 4)
         if (V == 8) k = combine_backward_kernel<RT, YT, 8>;
-    return launch(k, T, threads_for(dy.cols, V), 0, st, false, pos, w, K, (const YT*)dy.p, dy.stride, dy.cols,
+    const int all = ((dy.cols + V - 1) / V + 31) / 32 * 32;
+    return launch(k, T, all < 256 ? all : 256, 0, st, false, pos, w, K, (const YT*)dy.p, dy.stride, dy.cols,
                   (const RT*)rows.p, rows.stride, rows.rows, (RT*)(drows ? drows->p : nullptr), drows ? drows->stride : 0, dw);
 }
 
@@ -619,20 +624,20 @@ coli_status gather_entry(const int32_t* pos, const float* w, int T, int K, const
     REQUIRE(!overlap(y.p, y.bytes(), w, (size_t)T * K * 4), "weights and the output overlap");
     DeviceGuard guard(device);
     REQUIRE(guard.ok, "no such CUDA device");
-    cudaError_t e = launch_gather_sum(pos, w, T, K, rows, base ? &b : nullptr, y, st, false);
+    cudaError_t e = launch_gather_sum(pos, w, false, T, K, rows, base ? &b : nullptr, y, st, false);
     return e == cudaSuccess ? COLI_OK : block_cuda_fail(e, "combine");
 }
 
 }  // namespace
 
-cudaError_t launch_gather_sum(const int32_t* pos, const float* w, int T, int K, const Mat& rows, const Mat* base,
-                              const Mat& y, cudaStream_t st, bool dependent) {
+cudaError_t launch_gather_sum(const int32_t* pos, const float* w, bool skip_zero, int T, int K, const Mat& rows,
+                              const Mat* base, const Mat& y, cudaStream_t st, bool dependent) {
     const bool rf = rows.t == COLI_F32, yf = y.t == COLI_F32;
     using B = __nv_bfloat16;
-    if (rf) return yf ? gather_sum<float, float>(pos, w, T, K, rows, base, y, st, dependent)
-                      : gather_sum<float, B>(pos, w, T, K, rows, base, y, st, dependent);
-    return yf ? gather_sum<B, float>(pos, w, T, K, rows, base, y, st, dependent)
-              : gather_sum<B, B>(pos, w, T, K, rows, base, y, st, dependent);
+    if (rf) return yf ? gather_sum<float, float>(pos, w, skip_zero, T, K, rows, base, y, st, dependent)
+                      : gather_sum<float, B>(pos, w, skip_zero, T, K, rows, base, y, st, dependent);
+    return yf ? gather_sum<B, float>(pos, w, skip_zero, T, K, rows, base, y, st, dependent)
+              : gather_sum<B, B>(pos, w, skip_zero, T, K, rows, base, y, st, dependent);
 }
 
 }  // namespace coli

@@ -316,7 +316,8 @@ __global__ void __launch_bounds__(kThreads, 1) route_rows_kernel(const Rows a, c
         for (int i = threadIdx.x; i < ns + E; i += kThreads) refs[i] = none;
         __syncthreads();
         prefix(place, E, sums);
-        const int total = min(place[E], ns + E);  // (offsets that are not a plan of these slots may list too many)
+        // (offsets that are not a plan of these slots may list too many; even, as the places are)
+        const int total = min(place[E], ns + E) & ~1;
         auto put = [&](int i, int e, int q, float d) {
             if (d == 0.0f || (unsigned)e >= (unsigned)E) return;
             const int p = place[e] + (q - first[e]);
@@ -608,7 +609,7 @@ COLI_API coli_status coli_moe_route_backward(const float* router_w, int E, int H
     if (e != cudaSuccess) return block_cuda_fail(e, "route backward: logits");
     if (dx) {
         // few slots read fewer router rows than a slab of all of them holds
-        if ((int64_t)T * K < E) e = launch_gather_sum(ids, dlogits, T, K, mw, nullptr, mdx, st, true);
+        if ((int64_t)T * K < E) e = launch_gather_sum(ids, dlogits, true, T, K, mw, nullptr, mdx, st, true);
         else e = dtype == COLI_F32 ? route_dx<float>(ids, dlogits, mw, T, K, mdx, st)
                                    : route_dx<__nv_bfloat16>(ids, dlogits, mw, T, K, mdx, st);
         if (e != cudaSuccess) return block_cuda_fail(e, "route backward: dx");
