@@ -147,6 +147,21 @@ __device__ __forceinline__ void st16(void* p, uint4 r) {
 template <typename T, int V>
 struct Raw;
 template <>
+struct Raw<float, 8> {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const float* p) { a = ld16(p); b = ld16(p + 4); }
+    __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+        v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+    }
+    __device__ __forceinline__ void set(const float (&v)[8]) {
+        a = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        b = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+    }
+    __device__ __forceinline__ void store(float* p) const { st16(p, a); st16(p + 4, b); }
+};
+template <>
 struct Raw<__nv_bfloat16, 8> {
     uint4 a;
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = ld16(p); }

@@ -14,6 +14,7 @@ namespace {
 //   offsets[e] + (slots of e in earlier chunks) + (in earlier warps) + (before it in its warp),
 // so the order is (t, k) order and nothing depends on timing.
 // ---------------------------------------------------------------------------
+constexpr int kSms = 148;
 constexpr int kRankThreads = 1024;
 constexpr int kRankWarps = kRankThreads / 32;
 constexpr int kChunkSlots = 2048;  // slots of a chunk, until there are kMaxChunks of them
@@ -253,7 +254,7 @@ constexpr int kPieces = V >= 4 ? 1 : V == 2 ? 2 : 4;
 // rows[pos[t][k]] = x[t]: a thread reads its columns of a token once and writes
 // them K times. Bound by the K rows a token writes.
 template <typename XT, typename RT, int V>
-__global__ void __launch_bounds__(256) dispatch_rows_kernel(const XT* x, int64_t ldx, const int32_t* pos, int K, int H,
+__global__ void __launch_bounds__(128) dispatch_rows_kernel(const XT* x, int64_t ldx, const int32_t* pos, int K, int H,
                                                             RT* rows, int64_t ldr) {
     constexpr int N = kPieces<V>;
     const int t = blockIdx.x, step = blockDim.x * V;
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(256) dispatch_rows_kernel(const XT* x, int64_t
 // y[t] = base[t] + sum_k w[t][k] rows[pos[t][k]], the rows of eight slots in
 // flight at a time. Bound by the K rows a token reads.
 template <typename RT, typename YT, int V>
-__global__ void __launch_bounds__(256, sizeof(RT) == 4 ? 4 : 3) gather_sum_kernel(const int32_t* pos, const float* w, bool skip_zero, int K, const RT* rows,
+__global__ void __launch_bounds__(128, sizeof(RT) == 4 ? 8 : 6) gather_sum_kernel(const int32_t* pos, const float* w, bool skip_zero, int K, const RT* rows,
                                                          int64_t ldr, int n_rows, int H, const YT* base, int64_t ldb,
                                                          YT* y, int64_t ldy) {
     grid_wait();
@@ -395,34 +396,36 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const int32_t* po
 }
 
 // Threads of a block, and blocks of `pieces` pieces a thread, for rows of H
-// columns: blocks of up to 256 threads that share the columns evenly.
+// columns: blocks of up to 128 threads that share the columns evenly (combine of
+// 8192 x 8 x 6144 bf16 140 us, 6.5 TB/s; with up to 256 threads 146 us).
 struct Tiles {
     int threads, n;
 };
 Tiles tiles_of(int H, int V, int pieces = 1) {
-    const int all = (H + V * pieces - 1) / (V * pieces), n = (all + 255) / 256;
+    const int all = (H + V * pieces - 1) / (V * pieces), n = (all + 127) / 128;
     return {((all + n - 1) / n + 31) / 32 * 32, n};
 }
 
-// The largest of 8, 4, 2 and 1 columns a thread that all these rows take; 8
-// only of bf16 (of fp32, a warp's two accesses would lie 32 bytes apart and
-// read every 32-byte sector twice).
-int columns_of(const Mat& a, const Mat& b, const Mat* c = nullptr) {
+// The largest of 8, 4, 2 and 1 columns a thread that all these matrices take,
+// `rows` (the experts' side, most of the bytes) first; 8 only where they are
+// bf16 (of fp32, a warp's two accesses would lie 32 bytes apart and read every
+// 32-byte sector twice).
+int columns_of(const Mat& rows, const Mat& b, const Mat* c = nullptr) {
     for (int V : {8, 4, 2}) {
-        if (V == 8 && (a.t != COLI_BF16 || b.t != COLI_BF16)) continue;
-        if (a.takes(V) && b.takes(V) && (!c || c->takes(V))) return V;
+        if (V == 8 && rows.t != COLI_BF16) continue;
+        if (rows.takes(V) && b.takes(V) && (!c || c->takes(V))) return V;
     }
     return 1;
 }
 
 template <typename XT, typename RT>
 cudaError_t dispatch_rows(const Mat& x, const int32_t* pos, int T, int K, const Mat& rows, cudaStream_t st) {
-    const int V = columns_of(x, rows);
+    const int V = columns_of(rows, x);
     const Tiles g = tiles_of(x.cols, V, V >= 4 ? 1 : V == 2 ? 2 : 4);  // kPieces
     auto k = V == 4   ? dispatch_rows_kernel<XT, RT, 4>
              : V == 2 ? dispatch_rows_kernel<XT, RT, 2>
                       : dispatch_rows_kernel<XT, RT, 1>;
-    if constexpr (sizeof(XT) + sizeof(RT) == 4)
+    if constexpr (sizeof(RT) == 2)
         if (V == 8) k = dispatch_rows_kernel<XT, RT, 8>;
     return launch(k, dim3(T, g.n), g.threads, 0, st, true, (const XT*)x.p, x.stride, pos, K, x.cols, (RT*)rows.p,
                   rows.stride);
@@ -436,7 +439,7 @@ cudaError_t gather_sum(const int32_t* pos, const float* w, bool skip_zero, int T
     auto k = V == 4   ? gather_sum_kernel<RT, YT, 4>
              : V == 2 ? gather_sum_kernel<RT, YT, 2>
                       : gather_sum_kernel<RT, YT, 1>;
-    if constexpr (sizeof(RT) + sizeof(YT) == 4)
+    if constexpr (sizeof(RT) == 2)
         if (V == 8) k = gather_sum_kernel<RT, YT, 8>;
     return launch(k, dim3(T, g.n), g.threads, 0, st, dependent, pos, w, skip_zero, K, (const RT*)rows.p, rows.stride,
                   (int)(rows.rows < INT32_MAX ? rows.rows : INT32_MAX), y.cols, (const YT*)(base ? base->p : nullptr), base ? base->stride : 0, (YT*)y.p, y.stride);
@@ -445,14 +448,16 @@ cudaError_t gather_sum(const int32_t* pos, const float* w, bool skip_zero, int T
 template <typename RT, typename YT>
 cudaError_t combine_backward(const int32_t* pos, const float* w, int T, int K, const Mat& dy, const Mat& rows,
                              const Mat* drows, float* dw, cudaStream_t st) {
-    const int V = dw ? columns_of(dy, rows, drows) : columns_of(dy, *drows);
+    const int V = dw ? columns_of(rows, dy, drows) : columns_of(*drows, dy);
     auto k = V == 4   ? combine_backward_kernel<RT, YT, 4>
              : V == 2 ? combine_backward_kernel<RT, YT, 2>
                       : combine_backward_kernel<RT, YT, 1>;
-    if constexpr (sizeof(RT) + sizeof(YT) == 4)
+    if constexpr (sizeof(RT) == 2)
         if (V == 8) k = combine_backward_kernel<RT, YT, 8>;
-    const int all = ((dy.cols + V - 1) / V + 31) / 32 * 32;
-    return launch(k, T, all < 256 ? all : 256, 0, st, false, pos, w, K, (const YT*)dy.p, dy.stride, dy.cols,
+    // many tokens: small blocks, whose sums hold up fewer loads (2048 x 8 x 6144 bf16 71 us against 75 with
+    // 256 threads, x 4 x 2048 19 against 27); few: one token's columns at once (64 x 8 x 6144 5.8 against 8.3)
+    const int all = ((dy.cols + V - 1) / V + 31) / 32 * 32, most = T >= 4 * kSms ? 128 : 256;
+    return launch(k, T, all < most ? all : most, 0, st, false, pos, w, K, (const YT*)dy.p, dy.stride, dy.cols,
                   (const RT*)rows.p, rows.stride, rows.rows, (RT*)(drows ? drows->p : nullptr), drows ? drows->stride : 0, dw);
 }
 
@@ -563,11 +568,11 @@ __global__ void __launch_bounds__(kFewThreads) dispatch_few_kernel(const Few a, 
 
 template <typename XT, typename RT>
 cudaError_t dispatch_few(const Few& a, const Mat& x, const Mat& rows, cudaStream_t st) {
-    const int V = a.move ? columns_of(x, rows) : 4;
+    const int V = a.move ? columns_of(rows, x) : 4;
     auto k = V == 4   ? dispatch_few_kernel<XT, RT, 4>
              : V == 2 ? dispatch_few_kernel<XT, RT, 2>
                       : dispatch_few_kernel<XT, RT, 1>;
-    if constexpr (sizeof(XT) + sizeof(RT) == 4)
+    if constexpr (sizeof(RT) == 2)
         if (V == 8) k = dispatch_few_kernel<XT, RT, 8>;
     const int tiles = a.move ? (a.H + V * kFewThreads - 1) / (V * kFewThreads) : 1;
     return launch(k, dim3(a.T + 1, tiles), kFewThreads, 0, st, false, a, (const XT*)x.p, (RT*)rows.p);
