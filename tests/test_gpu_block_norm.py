@@ -10,7 +10,7 @@ Tolerances, in steps U = 2^-24 of the magnitudes that block_ref adds up:
 - ds: the mean of s q dn has 26 steps and two scales (2 x 25), 8 products: 100.
 - dy: a second mean over ds, the same again: 200.
 - sums over tokens: 200 for each value and one step for each of a block's rows
-  (T / 148 + 1 at most) and for the blocks (296 / 8 + 8): 250 + T / 148.
+  (T / 148 + 1 at most) and for the blocks (1184 / 16 + 16 = 90): 300 + T / 148.
 Then one rounding to the output's type.
 """
 import pytest
@@ -42,7 +42,7 @@ def both(coli, p):
 # T, H, layout
 SHAPES = [(1, 6144, "dense"), (1, 1, "dense"), (3, 7, "odd"), (5, 64, "apart"), (2, 8192, "dense"), (3, 8200, "dense"),
           (2, 16384, "apart"), (2, 16392, "dense"), (2, 1537, "dense"), (3, 8190, "odd"), (2, 8193, "dense"),
-          (300, 136, "dense"), (1, 65536, "dense"), (700, 40, "odd")]
+          (300, 136, "dense"), (1, 65536, "dense"), (700, 40, "odd"), (160, 516, "four"), (3, 2052, "four")]
 TYPES = [("f32", "f32", "f32"), ("bf16", "bf16", "bf16"), ("f32", "bf16", "bf16"), ("bf16", "f32", "f32")]
 
 
@@ -100,7 +100,7 @@ def check_backward(out, want, T, xt, yt):
     coeff = dict(dx=100, dy=200, dtoken=200)
     for name, got in out.items():
         value, mag = want[name]
-        ref.assert_near(got, value, mag, coeff.get(name, 250 + T / 148), name,
+        ref.assert_near(got, value, mag, coeff.get(name, 300 + T / 148), name,
                         DT[xt] if name == "dx" else DT[yt] if name == "dy" else torch.float32)
 
 
@@ -125,21 +125,61 @@ def test_backward(gpu, coli, T, H, layout, xt, yt, nt):
         check_backward(first, ref.Norm(None, b).backward(ref.d(s), None, ref.d(o), ref.d(dn)), T, xt, yt)
         last = run_backward(coli, a, None, s, y, dxo, None, u, xt, yt)
         check_backward(last, ref.Norm(a, None, u).backward(ref.d(s), ref.d(y), ref.d(dxo), None), T, xt, yt)
-    # in place: dx over dx_out, dy over y
+    # in place: dx over x_out, dy over dn; dx over dx_out, dy over y
     want = run_backward(coli, a, b, s, y, dxo, dn, u, xt, yt)
+    s2, dn2 = s.clone(), dn.clone()
+    got = run_backward(coli, a, b, s2, y, dxo, dn2, u, xt, yt, dx=s2, dy=dn2 if nt == yt else None)
+    for k in want:
+        assert torch.equal(want[k], got[k]), k
     got = run_backward(coli, a, b, s, y, dxo, dn, u, xt, yt, dx=dxo, dy=y)
     for k in want:
         assert torch.equal(want[k], got[k]), k
 
 
-@pytest.mark.parametrize("T,H", [(2048, 512), (1500, 1000), (449, 6144)])
-def test_sums_over_many_tokens(gpu, coli, T, H):
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("T,H", [(2048, 512), (1500, 1000), (449, 6144), (400, 8192), (700, 3001), (3000, 64)])
+def test_many_rows(gpu, coli, T, H, t):
+    """Blocks that take several rows each, with rings of one to four rows (8192 columns of fp32 leave room for
+    one row in the gradient), both ways; a block without post norm and without gate has one sum a row."""
     gen = torch.Generator().manual_seed(7)
-    s, y, dxo, dn = (torch.randn((T, H), generator=gen).to(gpu) for _ in range(4))
-    a, b = params(H, gpu, gen), params(H, gpu, gen)
+    s, y, dxo, dn = (torch.randn((T, H), generator=gen).to(gpu).to(DT[t]) for _ in range(4))
     u = torch.rand(T, generator=gen).to(gpu)
-    out = run_backward(coli, a, b, s, y, dxo, dn, u, "f32", "f32")
-    check_backward(out, ref.Norm(a, b, u).backward(ref.d(s), ref.d(y), ref.d(dxo), ref.d(dn)), T, "f32", "f32")
+    for post in (True, False):
+        a, b = params(H, gpu, gen, post=post, gate=post), params(H, gpu, gen)
+        r = ref.Norm(a, b, u)
+        out = run_backward(coli, a, b, s, y, dxo, dn, u, t, t)
+        check_backward(out, r.backward(ref.d(s), ref.d(y), ref.d(dxo), ref.d(dn)), T, t, t)
+        xo, n = torch.empty_like(s), torch.empty_like(s)
+        coli.block_norm(both(coli, a), both(coli, b), s, y, xo, n, u)
+        want, mag = r.x_out(ref.d(s), ref.d(y))
+        ref.assert_near(xo, want, mag, 32, "x_out", DT[t])
+        wn = r.n(ref.d(xo))
+        ref.assert_near(n, wn, wn.abs(), 28, "n", DT[t])
+        for prev, nxt, kw in ((None, b, dict(n=torch.empty_like(s))), (a, None, dict(x_out=torch.empty_like(s)))):
+            first = dict(x=xo) if prev is None else dict(x=s, y=y, token_gate=u)
+            coli.block_norm(both(coli, prev), both(coli, nxt), **first, **kw)
+            assert torch.equal(kw.get("n", n), n) and torch.equal(kw.get("x_out", xo), xo)
+
+
+def test_arrays_off_16_bytes(gpu, coli):
+    """Gains and gate that start on 4 bytes (the columns are then read one by one)."""
+    T, H = 5, 256
+    gen = torch.Generator().manual_seed(13)
+    x, y = torch.randn((T, H), generator=gen).to(gpu), torch.randn((T, H), generator=gen).to(gpu)
+    a, b = params(H, gpu, gen), params(H, gpu, gen)
+    off = lambda v: torch.cat([v.new_zeros(1), v])[1:]  # noqa: E731
+    res = []
+    for f in (lambda v: v, off):
+        aa = {k: f(v) if torch.is_tensor(v) else v for k, v in a.items()}
+        bb = {k: f(v) if torch.is_tensor(v) else v for k, v in b.items()}
+        xo, n = torch.empty_like(x), torch.empty_like(x)
+        coli.block_norm(both(coli, aa), both(coli, bb), x, y, xo, n)
+        res.append((xo, n, ref.Norm(aa, bb)))
+    for xo, n, r in res:
+        want, mag = r.x_out(ref.d(x), ref.d(y))
+        ref.assert_near(xo, want, mag, 32, "x_out")
+        wn = r.n(ref.d(xo))
+        ref.assert_near(n, wn, wn.abs(), 28, "n")
 
 
 @pytest.mark.parametrize("H", [512, 1001, 20000])
@@ -224,6 +264,6 @@ def test_gradients_against_differences(gpu, coli, post, token):
     dot = sum((ref.d(g[names[k]]) * v[k]).sum() for k in leaves)
     want = ref.Norm(a, b, u).backward(*(ref.d(t) for t in (xo, y, c1, c2)))
     mag = sum((want[names[k]][1] * v[k].abs()).sum() for k in leaves)
-    # 250 steps of each gradient's magnitude (x_out's own rounding, 32 steps, moves ds by as little), and
+    # 300 steps of each gradient's magnitude (x_out's own rounding, 32 steps, moves ds by as little), and
     # h^4 of the difference's remainder: h^4 = 2^-36
-    assert abs(dot - diff) <= 300 * ref.U * mag + 2.0 ** -36 * mag
+    assert abs(dot - diff) <= 340 * ref.U * mag + 2.0 ** -36 * mag

@@ -228,6 +228,11 @@ def test_block_stack(gpu, coli, T, cached):
     # a norm input off by 28 steps of 2^-24 moves the layer's 15-bit block-floating codes by one of their
     # steps at most, 2^-15 of a group's largest value, in few of them
     assert float((x.double() - want).abs().max() / want.abs().max()) < 1e-3
+    if T > 1:  # the first rows alone
+        part, before = x0.clone(), x0[T - 1].clone()
+        coli.block_stack_forward(layers, [coli.Block(**p) for p in par], part, work, n_tokens=T - 1)
+        assert torch.equal(part[T - 1], before) and not torch.equal(part[:T - 1], x0[:T - 1])
+        assert float((part[:T - 1] - x[:T - 1]).abs().max() / x.abs().max()) < 1e-3
     # unit parameters: the plain stack
     a, b = x0.clone(), x0.clone()
     coli.stack_forward(layers, a)

@@ -92,6 +92,8 @@ def view(shape, dtype, dev, layout, gen=None, fill=None):
     r, H = shape
     if layout == "dense":
         m = torch.empty((r, H), dtype=dtype, device=dev)
+    elif layout == "four":  # rows that start on 8 bytes (bf16) or 16 (fp32)
+        m = torch.full((r, H + 8), SENTINEL, device=dev).to(dtype)[:, 4:4 + H]
     elif layout == "apart":
         m = torch.full((r, H + 24), SENTINEL, device=dev).to(dtype)[:, 8:8 + H]
     else:
@@ -104,7 +106,8 @@ def view(shape, dtype, dev, layout, gen=None, fill=None):
 ROWS = [(1, 8, 256, 6144, "random", "dense"), (1, 1, 1, 1, "random", "dense"), (3, 2, 4, 7, "holes", "odd"),
         (17, 8, 32, 256, "holes", "apart"), (64, 8, 256, 2056, "random", "dense"), (40, 32, 64, 136, "holes", "odd"),
         (300, 8, 256, 264, "holes", "dense"), (33, 4, 7, 64, "none", "dense"), (20, 9, 3, 1000, "one", "apart"),
-        (2, 3, 5, 40000, "random", "dense"), (600, 4, 8, 1030, "holes", "dense")]
+        (2, 3, 5, 40000, "random", "dense"), (600, 4, 8, 1030, "holes", "dense"), (650, 3, 8, 516, "holes", "four"),
+        (7, 8, 16, 1028, "random", "four")]
 
 
 @pytest.mark.parametrize("xt,rt", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16"), ("bf16", "f32")])
