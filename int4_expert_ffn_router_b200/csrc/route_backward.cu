@@ -124,14 +124,26 @@ struct Columns<1> {
     __device__ __forceinline__ void add(float d, float2 (&acc)[1]) const { acc[0].x = fmaf(d, v, acc[0].x); }
 };
 
+struct Dx {
+    const int32_t* ids;
+    const float *dl, *wr;
+    int T, K, E, H, per, slabs, blocks;  // per: tokens of a block
+    int vec;
+    int64_t ldx;
+};
+
 template <typename XT, int VC>
-// (one block an SM: without the second bound the compiler saves registers for four)
-__global__ void __launch_bounds__(kThreads, 1) route_dx_kernel(const int32_t* ids, const float* dl, const float* wr, int T,
-                                                            int K, int E, int H, int per, bool vec, XT* dx, int64_t ldx) {
-    extern __shared__ __align__(16) float slab[];  // [E + 1][32 * VC], the last row zero
-    __shared__ __align__(16) SlotRef refs[kWarps][2][32];
+__device__ __forceinline__ void route_dx_block(const Dx& a, XT* dx, int bx, int by, unsigned char* shared) {
+    // [E + 1][32 * VC] columns of the router's rows, the last row zero; then each warp's two buffers of 32 slots
+    float* slab = reinterpret_cast<float*>(shared);
+    SlotRef* refs = reinterpret_cast<SlotRef*>(slab + (a.E + 1) * 32 * VC) + (threadIdx.x >> 5) * 64;
+    const int32_t* ids = a.ids;
+    const float *dl = a.dl, *wr = a.wr;
+    const int T = a.T, K = a.K, E = a.E, H = a.H, per = a.per;
+    const bool vec = a.vec;
+    const int64_t ldx = a.ldx;
     constexpr int C = 32 * VC;
-    const int c0 = blockIdx.x * C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c0 = bx * C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (vec) {
         for (int i = threadIdx.x; i < E * (C / 4); i += kThreads) {
             const int e = i / (C / 4), c = (i % (C / 4)) * 4;
@@ -147,8 +159,8 @@ __global__ void __launch_bounds__(kThreads, 1) route_dx_kernel(const int32_t* id
     grid_wait();  // dlogits
     // a warp's turn: its lanes hold the slots of G tokens, in groups of 8, 16 or 32 (zero rows behind the K-th)
     const int sh = K <= 8 ? 3 : K <= 16 ? 4 : 5, G = 32 >> sh, tg = lane >> sh, tk = lane & ((1 << sh) - 1);
-    const int t1 = min(T, (int)(blockIdx.y + 1) * per);
-    int t = blockIdx.y * per + warp * G;
+    const int t1 = min(T, (by + 1) * per);
+    int t = by * per + warp * G;
     auto fetch = [&](int at) {
         SlotRef r{E * C, 0.0f};
         if (tk < K && at + tg < t1) {
@@ -166,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) route_dx_kernel(const int32_t* id
     const float* col = slab + lane * VC;
     const int left = H - c0 - lane * VC;
     for (int flip = 0; t < t1; t += kWarps * G, flip ^= 1) {
-        SlotRef* ref = refs[warp][flip];
+        SlotRef* ref = refs + 32 * flip;
         ref[lane] = mine;
         __syncwarp();
         mine = fetch(t + kWarps * G);
@@ -217,7 +229,6 @@ __global__ void __launch_bounds__(kThreads, 1) route_dx_kernel(const int32_t* id
             }
         }
     }
-    grid_next();
 }
 
 // ---------------------------------------------------------------------------
@@ -264,27 +275,26 @@ __device__ __forceinline__ void prefix(int* v, int n, int* sums) {
 struct Rows {
     const int32_t *ids, *inv, *bound;
     const float* dl;
-    int T, K, E, H, chunk, n_chunks, per;
+    int T, K, E, H, chunk, n_chunks, per, slabs;
     int64_t ldx;
     int vec, vec_out;
     float *part, *part_b;  // NULL: not wanted
 };
 
 template <typename XT>
-__global__ void __launch_bounds__(kThreads, 1) route_rows_kernel(const Rows a, const XT* x) {
+__device__ __forceinline__ void route_rows_block(const Rows& a, const XT* x, int bx, int by, unsigned char* rows) {
     // rows [chunk + 1][256], the last one zero; slots [chunk * K + E]; place [E + 1] of an expert's first slot; first [E]
-    extern __shared__ __align__(16) unsigned char rows[];
     __shared__ int next, sums[kWarps];
     constexpr int C = kRowBytes / sizeof(XT), V = 16 / sizeof(XT), P = 4 / sizeof(XT);  // P pairs of columns a lane
     const int K = a.K, E = a.E, H = a.H, chunk = a.chunk;
     SlotRef* refs = reinterpret_cast<SlotRef*>(rows + (chunk + 1) * kRowBytes);
     int* place = reinterpret_cast<int*>(refs + chunk * K + E);
     int* first = place + E + 1;
-    const int c0 = blockIdx.x * C, lane = threadIdx.x & 31;
+    const int c0 = bx * C, lane = threadIdx.x & 31;
     const SlotRef none{chunk * kRowBytes, 0.0f};  // the zero row: an absent slot
     if (threadIdx.x < kRowBytes / 4) reinterpret_cast<int*>(rows + chunk * kRowBytes)[threadIdx.x] = 0;
     grid_wait();
-    const int k0 = blockIdx.y * a.per, k1 = min(a.n_chunks, k0 + a.per);
+    const int k0 = by * a.per, k1 = min(a.n_chunks, k0 + a.per);
     for (int k = k0; k < k1; ++k) {
         const int t0 = k * chunk, t1 = min(a.T, t0 + chunk), ns = (t1 - t0) * K;
         for (int e = threadIdx.x; e < E; e += kThreads) {
@@ -377,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) route_rows_kernel(const Rows a, c
                 }
                 if (q < q1) group(std::integral_constant<int, 1>(), q);
                 const int c = c0 + lane * 2 * P;
-                float* out = a.part + ((size_t)blockIdx.y * E + e) * H + c;
+                float* out = a.part + ((size_t)by * E + e) * H + c;
                 const bool more = k != k0;  // added to the sums of the chunks before
                 if (c < H) {
                     if (a.vec_out) {
@@ -405,17 +415,29 @@ __global__ void __launch_bounds__(kThreads, 1) route_rows_kernel(const Rows a, c
                     }
                 }
             }
-            if (a.part_b && blockIdx.x == 0) {
+            if (a.part_b && bx == 0) {
                 float b = 0.0f;
                 for (int q = q0 + lane; q < q1; q += 32) b += refs[q].d;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
-                float* out = a.part_b + (size_t)blockIdx.y * E + e;
+                float* out = a.part_b + (size_t)by * E + e;
                 if (lane == 0) *out = k != k0 ? *out + b : b;
             }
         }
         __syncthreads();
     }
+}
+
+// Both in one launch: they need the same preparation and nothing of one another,
+// and a launch of its own costs each 2 us. The blocks of dx come first. (One
+// block an SM: without the second bound the compiler saves registers for two.)
+template <typename XT, int VC>
+__global__ void __launch_bounds__(kThreads, 1) route_sums_kernel(const __grid_constant__ Dx d, const __grid_constant__ Rows r,
+                                                                 const XT* x, XT* dx) {
+    extern __shared__ __align__(16) unsigned char shared[];
+    const int b = blockIdx.x;
+    if (b < d.blocks) route_dx_block<XT, VC>(d, dx, b % d.slabs, b / d.slabs, shared);
+    else route_rows_block<XT>(r, x, (b - d.blocks) % r.slabs, (b - d.blocks) / r.slabs, shared);
     grid_next();
 }
 
@@ -484,49 +506,55 @@ Layout layout_of(const Cut& c, int T, int K, int E, int H) {
     return l;
 }
 
-template <typename XT>
-cudaError_t route_rows(Rows a, const Mat& x, const Cut& c, float* dwr, float* dbias, float* work, const Layout& l,
-                       cudaStream_t st) {
-    constexpr int C = kRowBytes / sizeof(XT);
-    const int H = a.H, E = a.E;
-    a.vec = x.vec() && H % (16 / sizeof(XT)) == 0;
-    // one split writes the result itself, several their parts
-    a.part = !dwr ? nullptr : c.splits > 1 ? work : dwr;
-    a.part_b = !dbias ? nullptr : c.splits > 1 ? work + l.part_b : dbias;
-    a.vec_out = H % 4 == 0 && ((uintptr_t)a.part & 15u) == 0;
-    const size_t smem = (size_t)(c.chunk + 1) * kRowBytes + ((size_t)c.chunk * a.K + E) * 8 + (size_t)(2 * E + 1) * 4;
-    cudaError_t e = cudaFuncSetAttribute(route_rows_kernel<XT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    e = launch(route_rows_kernel<XT>, dim3(dwr ? (H + C - 1) / C : 1, c.splits), kThreads, smem, st, true, a, (const XT*)x.p);
-    if (e != cudaSuccess || c.splits == 1) return e;
-    const int n = E * H;
-    const bool v4 = H % 4 == 0 && (((uintptr_t)dwr | (uintptr_t)work) & 15u) == 0;
-    const int V = v4 ? 4 : 1, blocks = dwr ? (n / V + 255) / 256 : 1, need = (E + 255) / 256;
-    return launch(v4 ? route_sum_kernel<4> : route_sum_kernel<1>, blocks > need ? blocks : need, 256, 0, st, true,
-                  (const float*)a.part, c.splits, n, dwr, (const float*)a.part_b, E, dbias);
-}
-
-// Columns of a slab of all E router rows (and the zero row) in shared memory.
+// Columns of a slab of all E router rows (and the zero row) in shared memory, in warps' widths.
 int slab_columns(int E) {
     for (int vc : {4, 2}) if ((size_t)(E + 1) * 32 * vc * 4 <= 200 * 1024) return vc;
     return 1;
 }
 
+// dx (dx.p NULL: not wanted here) and the parts of drouter_w and dbias (NULL: not wanted).
 template <typename XT>
-cudaError_t route_dx(const int32_t* ids, const float* dl, const Mat& wr, int T, int K, const Mat& dx, cudaStream_t st) {
-    const int E = (int)wr.rows, H = wr.cols, vc = slab_columns(E), C = 32 * vc;
-    const int slabs = (H + C - 1) / C;
-    int n = kSms / slabs;
-    if (n > (T + kWarps - 1) / kWarps) n = (T + kWarps - 1) / kWarps;
-    if (n < 1) n = 1;
-    const int per = (T + n - 1) / n;
-    const bool vec = H % 4 == 0 && wr.vec() && dx.vec();
-    const size_t smem = (size_t)(E + 1) * C * 4;
-    auto k = vc == 4 ? route_dx_kernel<XT, 4> : vc == 2 ? route_dx_kernel<XT, 2> : route_dx_kernel<XT, 1>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+cudaError_t route_sums(const Prep& p, const Mat& wr, const Mat& x, const Mat& dx, const Cut& c, float* dwr, float* dbias,
+                       float* work, const Layout& l, cudaStream_t st) {
+    constexpr int C = kRowBytes / sizeof(XT);
+    const int T = p.T, K = p.K, E = p.E, H = x.cols;
+    size_t smem = 0;
+    const int vc = slab_columns(E);
+    Dx d{p.ids, p.dl, (const float*)wr.p, T, K, E, H, 0, 1, 0, 0, dx.stride};
+    if (dx.p) {
+        d.slabs = (H + 32 * vc - 1) / (32 * vc);
+        int n = kSms / d.slabs;
+        if (n > (T + kWarps - 1) / kWarps) n = (T + kWarps - 1) / kWarps;
+        if (n < 1) n = 1;
+        d.per = (T + n - 1) / n;
+        d.blocks = d.slabs * ((T + d.per - 1) / d.per);
+        d.vec = H % 4 == 0 && wr.vec() && dx.vec();
+        smem = (size_t)(E + 1) * 32 * vc * 4 + kWarps * 64 * sizeof(SlotRef);
+    }
+    Rows r{p.ids, p.inv, p.bound, p.dl, T, K, E, H, c.chunk, c.n_chunks, c.per, 1, x.stride};
+    int blocks = d.blocks;
+    if (dwr || dbias) {
+        r.vec = x.vec() && H % (16 / sizeof(XT)) == 0;
+        // one split writes the result itself, several their parts
+        r.part = !dwr ? nullptr : c.splits > 1 ? work : dwr;
+        r.part_b = !dbias ? nullptr : c.splits > 1 ? work + l.part_b : dbias;
+        r.vec_out = H % 4 == 0 && ((uintptr_t)r.part & 15u) == 0;
+        r.slabs = dwr ? (H + C - 1) / C : 1;
+        blocks += r.slabs * c.splits;
+        const size_t need = (size_t)(c.chunk + 1) * kRowBytes + ((size_t)c.chunk * K + E) * 8 + (size_t)(2 * E + 1) * 4;
+        if (need > smem) smem = need;
+    }
+    if (blocks == 0) return cudaSuccess;
+    auto k = vc == 4 ? route_sums_kernel<XT, 4> : vc == 2 ? route_sums_kernel<XT, 2> : route_sums_kernel<XT, 1>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch(k, dim3(slabs, (T + per - 1) / per), kThreads, smem, st, true, ids, dl, (const float*)wr.p, T, K, E, H, per,
-                  vec, (XT*)dx.p, dx.stride);
+    e = launch(k, blocks, kThreads, smem, st, true, d, r, (const XT*)x.p, (XT*)dx.p);
+    if (e != cudaSuccess || c.splits == 1 || !(dwr || dbias)) return e;
+    const int n = E * H;
+    const bool v4 = H % 4 == 0 && (((uintptr_t)dwr | (uintptr_t)work) & 15u) == 0;
+    const int V = v4 ? 4 : 1, sums = dwr ? (n / V + 255) / 256 : 1, need = (E + 255) / 256;
+    return launch(v4 ? route_sum_kernel<4> : route_sum_kernel<1>, sums > need ? sums : need, 256, 0, st, true,
+                  (const float*)r.part, c.splits, n, dwr, (const float*)r.part_b, E, dbias);
 }
 
 #define REQUIRE(cond, msg)                                \
@@ -610,21 +638,15 @@ COLI_API coli_status coli_moe_route_backward(const float* router_w, int E, int H
     const int n_bound = rows ? ((c.n_chunks + 1) * E + 255) / 256 : 0;
     e = launch(route_prep_kernel, p.n_tok + p.n_inv + n_bound, 256, 0, st, false, p);
     if (e != cudaSuccess) return block_cuda_fail(e, "route backward: logits");
-    if (dx) {
-        // few slots read fewer router rows than a slab of all of them holds
-        if ((int64_t)T * K < E) e = launch_gather_sum(ids, dlogits, true, T, K, mw, nullptr, mdx, st, true);
-        else e = dtype == COLI_F32 ? route_dx<float>(ids, dlogits, mw, T, K, mdx, st)
-                                   : route_dx<__nv_bfloat16>(ids, dlogits, mw, T, K, mdx, st);
+    // few slots read fewer router rows than a slab of all of them holds
+    const bool gather = dx && (int64_t)T * K < E;
+    if (gather) {
+        e = launch_gather_sum(ids, dlogits, true, T, K, mw, nullptr, mdx, st, true);
         if (e != cudaSuccess) return block_cuda_fail(e, "route backward: dx");
     }
-    if (rows) {
-        Rows r{};
-        r.ids = ids, r.inv = p.inv, r.bound = p.bound, r.dl = dlogits;
-        r.T = T, r.K = K, r.E = E, r.H = H, r.chunk = c.chunk, r.n_chunks = c.n_chunks, r.per = c.per;
-        r.ldx = x_stride;
-        e = dtype == COLI_F32 ? route_rows<float>(r, mx, c, drouter_w, dbias, (float*)work, l, st)
-                              : route_rows<__nv_bfloat16>(r, mx, c, drouter_w, dbias, (float*)work, l, st);
-        if (e != cudaSuccess) return block_cuda_fail(e, "route backward: rows");
-    }
+    const Mat to{gather ? nullptr : dx, dtype, T, H, dx_stride};
+    e = dtype == COLI_F32 ? route_sums<float>(p, mw, mx, to, c, drouter_w, dbias, (float*)work, l, st)
+                          : route_sums<__nv_bfloat16>(p, mw, mx, to, c, drouter_w, dbias, (float*)work, l, st);
+    if (e != cudaSuccess) return block_cuda_fail(e, "route backward: sums");
     return COLI_OK;
 }

@@ -32,16 +32,15 @@ def formula(wr, x, ids, w, dw):
     Dl = w.abs() * (dw.abs() + (w * dw).abs().sum(1, keepdim=True))
     z = lambda *s: torch.zeros(s, dtype=torch.float64)  # noqa: E731
     dx, Dx, dwr, Dwr, db, Db = z(T, H), z(T, H), z(E, H), z(E, H), z(E), z(E)
-    for t in range(T):
-        for k in range(K):
-            if on[t, k]:
-                e = int(ids[t, k])
-                dx[t] += dl[t, k] * wr[e]
-                Dx[t] += Dl[t, k] * wr[e].abs()
-                dwr[e] += dl[t, k] * x[t]
-                Dwr[e] += Dl[t, k] * x[t].abs()
-                db[e] += dl[t, k]
-                Db[e] += Dl[t, k]
+    e = torch.where(on, ids, torch.zeros_like(ids)).long()  # a slot that is off has dl and Dl 0
+    for k in range(K):
+        d, D = dl[:, k:k + 1], Dl[:, k:k + 1]
+        dx += d * wr[e[:, k]]
+        Dx += D * wr[e[:, k]].abs()
+        dwr.index_add_(0, e[:, k], d * x)
+        Dwr.index_add_(0, e[:, k], D * x.abs())
+        db.index_add_(0, e[:, k], dl[:, k])
+        Db.index_add_(0, e[:, k], Dl[:, k])
     return dict(dlogits=(dl, Dl), dx=(dx, Dx), dwr=(dwr, Dwr), dbias=(db, Db))
 
 
@@ -63,7 +62,10 @@ def run(coli, wr, x, ids, w, dw, dev, layout="dense", only=("dx", "dwr", "dbias"
 CASES = [(1, 1, 1, 1, "random", "dense"), (1, 8, 256, 6144, "random", "dense"), (64, 2, 16, 512, "random", "dense"),
          (33, 4, 7, 130, "holes", "odd"), (50, 32, 40, 264, "holes", "apart"), (300, 8, 64, 72, "holes", "dense"),
          (700, 3, 2, 100, "one", "dense"), (20, 4, 9, 64, "none", "dense"), (1200, 8, 256, 256, "random", "dense"),
-         (5, 2, 1024, 2056, "random", "dense")]
+         (5, 2, 1024, 2056, "random", "dense"),
+         # chunks that fill a block's shared memory; several chunks to a split
+         (690, 8, 256, 19072, "random", "dense"), (2048, 8, 256, 6144, "holes", "dense"), (400, 32, 1024, 6100, "holes", "dense"),
+         (3000, 8, 32, 19000, "random", "dense"), (130, 1, 400, 128, "random", "four"), (2000, 16, 801, 256, "random", "dense")]
 
 
 @pytest.mark.parametrize("xt", ["f32", "bf16"])
