@@ -59,7 +59,6 @@ struct Mat {
     bool aligned(size_t n) const { return ((uintptr_t)p % n) == 0; }
     // rows start on n-byte boundaries (one row: its start alone)
     bool starts(size_t n) const { return aligned(n) && (rows <= 1 || (size_t)stride * dtype_size(t) % n == 0); }
-    bool vec() const { return starts(16); }
     // V values a thread can be read and written at a time, by accesses of up to 16 bytes
     bool takes(int V) const {
         const size_t n = V * dtype_size(t);
@@ -120,6 +119,13 @@ cudaError_t launch_clusters(int cluster, void (*kernel)(P...), dim3 grid, dim3 b
 template <typename... P, typename... A>
 cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, bool dependent, A... args) {
     return launch_clusters(1, kernel, grid, block, smem, st, dependent, args...);
+}
+// Lets `kernel` take dynamic shared memory of up to `most` bytes. The limit is one
+// for all callers of a kernel on a device, so it is the most that any call
+// takes: of two threads' calls one would otherwise lower it under the other's launch.
+template <typename... P>
+cudaError_t allow_shared(void (*kernel)(P...), size_t most) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
 }
 // Waits until the kernels before this one have finished and their writes can be read.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

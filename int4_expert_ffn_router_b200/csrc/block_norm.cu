@@ -35,18 +35,8 @@ __device__ __forceinline__ bool sum_ok(float ss, float eps) { return ss <= 3e37f
 __device__ __forceinline__ float rms_scale(float ss, int H, float eps) { return rsqrtf(ss / (float)H + eps); }
 __device__ __forceinline__ float rms_scale(double ss, int H, float eps) { return (float)(1.0 / sqrt(ss / H + (double)eps)); }
 
-template <int V>
-__device__ __forceinline__ void load_gain(const float* g, int c, float (&v)[V]) {
-    if (!g) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = 1.0f;
-    } else if constexpr (V == 8) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(g + c)), b = __ldg(reinterpret_cast<const float4*>(g + c) + 1);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-        v[0] = __ldg(g + c);
-    }
-}
+// A column's gain or gate (NULL: 1).
+__device__ __forceinline__ float gain(const float* g, int c) { return g ? __ldg(g + c) : 1.0f; }
 
 // ---------------------------------------------------------------------------
 // A thread holds N pieces of V columns of a row: V = 8 where all rows are bf16,
@@ -473,12 +463,10 @@ __global__ void __launch_bounds__(1024) block_norm_wide_kernel(NormArgs a) {
             Raw<YT, 1> ry;
             rx.load(x + c);
             ry.load(y + c);
-            float vx[1], vy[1], p[1], g[1];
+            float vx[1], vy[1];
             rx.get(vx);
             ry.get(vy);
-            load_gain<1>(a.post, c, p);
-            load_gain<1>(a.gate, c, g);
-            vx[0] = fmaf(scale * g[0], vy[0] * rho * p[0], a.xs * vx[0]);
+            vx[0] = fmaf(scale * gain(a.gate, c), vy[0] * rho * gain(a.post, c), a.xs * vx[0]);
             rx.set(vx);
             rx.store(xo + c);
             rx.get(vx);
@@ -512,10 +500,9 @@ __global__ void __launch_bounds__(1024) block_norm_wide_kernel(NormArgs a) {
     for (int c = threadIdx.x; c < H; c += blockDim.x) {
         Raw<XT, 1> rx;
         rx.load(x + c);
-        float v[1], q[1];
+        float v[1];
         rx.get(v);
-        load_gain<1>(a.pre, c, q);
-        v[0] = v[0] * r * q[0];
+        v[0] = v[0] * r * gain(a.pre, c);
         Raw<NT, 1> out;
         out.set(v);
         out.store((NT*)a.n + (size_t)t * a.ldn + c);
@@ -813,11 +800,10 @@ __global__ void __launch_bounds__(1024) block_norm_backward_wide_kernel(NormArgs
         };
         double w[3] = {0.0, 0.0, 0.0};
         for (int c = threadIdx.x; c < H; c += blockDim.x) {
-            float s, y, n, o, q[1];
+            float s, y, n, o;
             row(c, s, y, n, o);
-            load_gain<1>(a.pre, c, q);
             w[0] += (double)s * s;
-            w[1] += (double)s * q[0] * n;
+            w[1] += (double)s * gain(a.pre, c) * n;
             w[2] += (double)y * y;
         }
         block_sum<double, 3>(w, red64[0]);
@@ -828,19 +814,14 @@ __global__ void __launch_bounds__(1024) block_norm_backward_wide_kernel(NormArgs
         float m2 = 0.0f;
         for (int round = 0; round < 2; ++round) {
             for (int c = threadIdx.x; c < H; c += blockDim.x) {
-                float s, y, n, o, q[1], b[1] = {0.0f}, p[1];
+                float s, y, n, o;
                 row(c, s, y, n, o);
-                load_gain<1>(a.pre, c, q);
-                if (a.has_prev) {
-                    load_gain<1>(a.gate, c, b);
-                    load_gain<1>(a.post, c, p);
-                    b[0] *= a.ys * p[0];
-                }
+                const float b = a.has_prev ? gain(a.gate, c) * (a.ys * gain(a.post, c)) : 0.0f;
                 const float sh = s * r;
-                if (a.has_next) o = fmaf(r, fmaf(-sh, m1, q[0] * n), o);
+                if (a.has_next) o = fmaf(r, fmaf(-sh, m1, gain(a.pre, c) * n), o);
                 const float yh = y * rho;
                 if (round == 0) {
-                    v[0] += (double)b[0] * yh * o;
+                    v[0] += (double)b * yh * o;
                     if (part) {
                         part[c] = first ? sh * n : fmaf(sh, n, part[c]);
                         part[H + c] = first ? u * yh * o : fmaf(u * yh, o, part[H + c]);
@@ -853,7 +834,7 @@ __global__ void __launch_bounds__(1024) block_norm_backward_wide_kernel(NormArgs
                         out.store((XT*)a.dx + (size_t)t * a.lddx + c);
                     }
                     if (a.dy) {
-                        f[0] = rho * fmaf(-yh, m2, u * b[0] * o);
+                        f[0] = rho * fmaf(-yh, m2, u * b * o);
                         Raw<YT, 1> out;
                         out.set(f);
                         out.store((YT*)a.dy + (size_t)t * a.lddy + c);
@@ -928,9 +909,10 @@ int grid_of(int T, int H, bool fwd) {
     const int g = kSms * blocks_per_sm(shape_of(H, H % 8 == 0 ? 8 : H % 4 == 0 ? 4 : 2).threads, fwd);
     return T < g ? T : g;
 }
+constexpr size_t kRingBytes = 200 * 1024;  // of an SM's shared memory
 // Ring slots of `row` bytes (at most 128 KB) that fit beside the other blocks of an SM.
 int stages_of(size_t row, int threads, int rows, bool fwd) {
-    const size_t n = 200 * 1024 / blocks_per_sm(threads, fwd) / row;
+    const size_t n = kRingBytes / blocks_per_sm(threads, fwd) / row;
     return n < 1 || rows < 2 ? 1 : n > 4 ? 4 : (int)n;
 }
 
@@ -942,7 +924,7 @@ cudaError_t launch_rows(Kernel k, NormArgs& a, const Shape& s, size_t col_bytes,
     a.stages = row ? stages_of(row, s.threads, (a.T + grid - 1) / grid, fwd) : 0;
     const size_t smem = a.stages * row;
     if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = allow_shared(k, kRingBytes);
         if (e != cudaSuccess) return e;
     }
     return launch(k, grid, s.threads, smem, st, false, a);

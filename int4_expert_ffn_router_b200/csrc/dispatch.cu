@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kRankThreads) dispatch_rank_kernel(const int32
     grid_next();
 }
 
+constexpr int kMaxExperts = 1024;
 size_t rank_smem(int E) { return sizeof(int32_t) * ((size_t)kRankWarps * E + 32); }
 
 // ---------------------------------------------------------------------------
@@ -657,7 +658,7 @@ cudaError_t launch_gather_sum(const int32_t* pos, const float* w, bool skip_zero
 using namespace coli;
 
 COLI_API int64_t coli_moe_dispatch_workspace(int T, int K, int E) {
-    if (check_slots(T, K) || E < 1 || E > 1024) return -1;
+    if (check_slots(T, K) || E < 1 || E > kMaxExperts) return -1;
     const int64_t n = (int64_t)T * K;
     return n > kClusterSlots ? (int64_t)chunks_of(n).n * E * 4 : 0;
 }
@@ -667,7 +668,7 @@ COLI_API coli_status coli_moe_dispatch(const int32_t* ids, int T, int K, int E, 
                                        int32_t* slot, void* rows, coli_dtype rows_dtype, int64_t rows_stride,
                                        int64_t n_rows, void* work, int64_t work_bytes, int device, coli_stream stream) {
     TRY_ARG(check_slots(T, K));
-    REQUIRE(E >= 1 && E <= 1024, "n_experts must be in [1, 1024]");
+    REQUIRE(E >= 1 && E <= kMaxExperts, "n_experts must be in [1, 1024]");
     REQUIRE(counts && offsets, "counts or offsets is NULL");
     REQUIRE(T == 0 || (ids && pos && slot), "ids, pos or slot is NULL");
     REQUIRE(aligned4(ids) && aligned4(counts) && aligned4(offsets) && aligned4(pos) && aligned4(slot),
@@ -712,7 +713,7 @@ COLI_API coli_status coli_moe_dispatch(const int32_t* ids, int T, int K, int E, 
     if (n <= kClusterSlots) {
         const int chunk = (int)((n + kCluster * kRankThreads - 1) / (kCluster * kRankThreads)) * kRankThreads;
         const size_t smem = rank_smem(E) + (size_t)E * 4;
-        e = cudaFuncSetAttribute(dispatch_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = allow_shared(dispatch_sort_kernel, rank_smem(kMaxExperts) + kMaxExperts * 4);
         if (e != cudaSuccess) return block_cuda_fail(e, "dispatch: shared memory");
         e = launch_clusters(kCluster, dispatch_sort_kernel, kCluster, kRankThreads, smem, st, false, ids, (int)n, E, chunk,
                             counts, offsets, pos, slot);
@@ -721,7 +722,7 @@ COLI_API coli_status coli_moe_dispatch(const int32_t* ids, int T, int K, int E, 
         e = launch(dispatch_count_kernel, c.n, kRankThreads, 0, st, false, ids, (int)n, E, c.size, (int32_t*)work);
         if (e != cudaSuccess) return block_cuda_fail(e, "dispatch: count");
         const size_t smem = rank_smem(E);
-        e = cudaFuncSetAttribute(dispatch_rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = allow_shared(dispatch_rank_kernel, rank_smem(kMaxExperts));
         if (e != cudaSuccess) return block_cuda_fail(e, "dispatch: shared memory");
         e = launch(dispatch_rank_kernel, c.n, kRankThreads, smem, st, true, ids, (int)n, E, c.size, (const int32_t*)work,
                    counts, offsets, pos, slot);

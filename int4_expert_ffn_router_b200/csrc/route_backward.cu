@@ -244,7 +244,8 @@ __device__ __forceinline__ void route_dx_block(const Dx& a, XT* dx, int bx, int 
 // walked its slots took 1200: the hottest expert has most tokens.)
 // ---------------------------------------------------------------------------
 constexpr int kRowBytes = 256;
-constexpr int kRoom = 224 * 1024;  // shared memory of a block
+constexpr int kRoom = 224 * 1024;        // shared memory of a chunk
+constexpr int kMostShared = 226 * 1024;  // of any block: over all E and K, 229,364 bytes are the most
 constexpr int kFirst = 6;           // slots a thread asks for at once (all of a chunk's, with K <= 8)
 
 // Most tokens of a chunk: their rows, one zero row, their slots (an even number of each expert's), and two
@@ -528,13 +529,13 @@ cudaError_t route_sums(const Prep& p, const Mat& wr, const Mat& x, const Mat& dx
         if (n < 1) n = 1;
         d.per = (T + n - 1) / n;
         d.blocks = d.slabs * ((T + d.per - 1) / d.per);
-        d.vec = H % 4 == 0 && wr.vec() && dx.vec();
+        d.vec = H % 4 == 0 && wr.starts(16) && dx.starts(16);
         smem = (size_t)(E + 1) * 32 * vc * 4 + kWarps * 64 * sizeof(SlotRef);
     }
     Rows r{p.ids, p.inv, p.bound, p.dl, T, K, E, H, c.chunk, c.n_chunks, c.per, 1, x.stride};
     int blocks = d.blocks;
     if (dwr || dbias) {
-        r.vec = x.vec() && H % (16 / sizeof(XT)) == 0;
+        r.vec = x.starts(16) && H % (16 / sizeof(XT)) == 0;
         // one split writes the result itself, several their parts
         r.part = !dwr ? nullptr : c.splits > 1 ? work : dwr;
         r.part_b = !dbias ? nullptr : c.splits > 1 ? work + l.part_b : dbias;
@@ -546,7 +547,7 @@ cudaError_t route_sums(const Prep& p, const Mat& wr, const Mat& x, const Mat& dx
     }
     if (blocks == 0) return cudaSuccess;
     auto k = vc == 4 ? route_sums_kernel<XT, 4> : vc == 2 ? route_sums_kernel<XT, 2> : route_sums_kernel<XT, 1>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_shared(k, kMostShared);
     if (e != cudaSuccess) return e;
     e = launch(k, blocks, kThreads, smem, st, true, d, r, (const XT*)x.p, (XT*)dx.p);
     if (e != cudaSuccess || c.splits == 1 || !(dwr || dbias)) return e;

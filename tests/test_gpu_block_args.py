@@ -135,3 +135,38 @@ def test_two_streams_with_workspaces_of_their_own(gpu, coli):
     torch.cuda.synchronize()
     for k in ("dx", "dy", "dq", "dp"):
         assert torch.equal(res[0][k], res[1][k])
+
+
+def test_calls_of_several_threads(gpu, coli):
+    """Calls of one kernel with different amounts of shared memory, made at the same time."""
+    from concurrent.futures import ThreadPoolExecutor
+
+    def work(i):
+        E, T, K, H = (4, 16, 300, 1024)[i], (700, 4000, 1500, 900)[i], (3, 8, 4, 2)[i], (1024, 4096, 512, 2048)[i]
+        g = torch.Generator().manual_seed(i)
+        ids = torch.stack([torch.randperm(E, generator=g)[:K] for _ in range(T)]).to(torch.int32).to(gpu)
+        x, y, o = (torch.randn((T, H), generator=g).to(gpu) for _ in range(3))
+        w, dw = (torch.randn((T, K), generator=g).to(gpu) for _ in range(2))
+        wr = torch.randn((E, H), generator=g).to(gpu)
+        st, first = torch.cuda.Stream(gpu), None
+        i32 = dict(dtype=torch.int32, device=gpu)
+        bufs = [torch.zeros(n, **i32) for n in (E, E + 1, (T, K), T * K)]
+        dl, dx, dwr, db = (torch.zeros(n, device=gpu) for n in ((T, K), (T, H), (E, H), (E,)))
+        xo, n, gx, gy = (torch.zeros_like(x) for _ in range(4))
+        dwork = torch.zeros(coli.dispatch_workspace(T, K, E), dtype=torch.uint8, device=gpu)
+        rwork = torch.zeros(coli.route_backward_workspace(T, K, E, H), dtype=torch.uint8, device=gpu)
+        torch.cuda.synchronize()
+        for _ in range(200):
+            counts, offsets, pos, slot = bufs
+            coli.dispatch(ids, None, E, counts, offsets, pos, slot, None, dwork, stream=st)
+            coli.route_backward(wr, x, ids, w, dw, offsets, slot, dl, dx, dwr, db, rwork, stream=st)
+            coli.block_norm(coli.Block(), coli.Block(), x, y, xo, n, stream=st)
+            coli.block_norm_backward(coli.Block(), coli.Block(), x, y, o, x, gx, gy, stream=st)
+            st.synchronize()
+            if first is None:
+                first = [t.clone() for t in (*bufs, dl, dx, dwr, db, xo, n, gx, gy)]
+                torch.cuda.synchronize()
+        return all(torch.equal(a, b) for a, b in zip(first, (*bufs, dl, dx, dwr, db, xo, n, gx, gy)))
+
+    with ThreadPoolExecutor(4) as pool:
+        assert all(pool.map(work, range(4)))
