@@ -86,9 +86,7 @@ __global__ void __launch_bounds__(kRankThreads) dispatch_rank_kernel(const int32
     for (int i0 = w0; i0 < w1; i0 += 32) {
         const int i = i0 + lane;
         const int e = i < w1 ? ids[i] : -1;
-        const unsigned m = __match_any_sync(0xffffffffu, e);
-        if ((unsigned)e < (unsigned)E && lane == __ffs(m) - 1) wcnt[warp * E + e] += __popc(m);
-        __syncwarp();
+        if ((unsigned)e < (unsigned)E) atomicAdd(wcnt + warp * E + e, 1);  // an integer count: the order does not matter
     }
     __syncthreads();
     int mine = 0;  // this chunk's slots of expert e = threadIdx.x, its warps' counts made exclusive
@@ -147,9 +145,12 @@ size_t rank_smem(int E) { return sizeof(int32_t) * ((size_t)kRankWarps * E + 32)
 // The same sort in one launch for up to kClusterSlots slots: a cluster of eight
 // blocks, a chunk each, which read each other's counts from shared memory. A
 // warp's first 64 slots stay in registers between the two passes. With the rows
-// (256 columns of bf16), dispatch took 11.8 us for 24000 slots where the two
-// launches above took 12.8, but 15.5 against 13.6 for 32768: eight blocks are
-// then too few.
+// (256 columns of bf16), dispatch takes 12.2 us for 28000 slots where the two
+// launches above take 12.4, but 12.9 against 12.1 for 32768 and 17.9 against 14.5
+// for 48000: eight blocks are then too few. Bound by its steps' latency: for
+// 16384 slots 1.2 us until the slots are read, 2 of barrier (1.5 of them the
+// warps' matching), 1.5 of the others' counts and the scan, 1.1 of placing.
+// Counting by matching lanes too, as placing does, took 2.4 us more.
 // ---------------------------------------------------------------------------
 constexpr int kCluster = 8;
 constexpr int kClusterSlots = 24576;
@@ -184,9 +185,7 @@ __global__ void __launch_bounds__(kRankThreads, 1) dispatch_sort_kernel(const in
     for (int i = threadIdx.x; i < kRankWarps * E; i += kRankThreads) wcnt[i] = 0;
     __syncthreads();
     auto count = [&](int e) {
-        const unsigned m = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && lane == __ffs(m) - 1) wcnt[warp * E + e] += __popc(m);
-        __syncwarp();
+        if (e >= 0) atomicAdd(wcnt + warp * E + e, 1);  // an integer count: the order does not matter
     };
     count(kept[0]);
     if (per > 32) count(kept[1]);
@@ -205,6 +204,8 @@ __global__ void __launch_bounds__(kRankThreads, 1) dispatch_sort_kernel(const in
         tot[threadIdx.x] = mine;
     }
     cluster_arrive();
+    // the lanes with the same expert, while the other blocks come
+    const unsigned same[2] = {__match_any_sync(0xffffffffu, kept[0]), __match_any_sync(0xffffffffu, kept[1])};
     cluster_wait();
     int total = 0, before = 0;  // over all chunks; over the chunks before this one
     if (threadIdx.x < E) {
@@ -228,8 +229,7 @@ __global__ void __launch_bounds__(kRankThreads, 1) dispatch_sort_kernel(const in
     }
     if (rank == 0 && threadIdx.x == 0) offsets[E] = all;
     __syncthreads();
-    auto place = [&](int i, int e) {
-        const unsigned m = __match_any_sync(0xffffffffu, e);
+    auto place = [&](int i, int e, unsigned m) {
         int q = -1;
         if (e >= 0) {
             q = wcnt[warp * E + e] + __popc(m & ((1u << lane) - 1u));
@@ -240,9 +240,12 @@ __global__ void __launch_bounds__(kRankThreads, 1) dispatch_sort_kernel(const in
         if (e >= 0 && lane == __ffs(m) - 1) wcnt[warp * E + e] += __popc(m);
         __syncwarp();
     };
-    place(w0 + lane, kept[0]);
-    if (per > 32) place(w0 + 32 + lane, kept[1]);
-    for (int i0 = w0 + 64; i0 < w0 + per; i0 += 32) place(i0 + lane, fetch(i0 + lane));
+    place(w0 + lane, kept[0], same[0]);
+    if (per > 32) place(w0 + 32 + lane, kept[1], same[1]);
+    for (int i0 = w0 + 64; i0 < w0 + per; i0 += 32) {
+        const int e = fetch(i0 + lane);
+        place(i0 + lane, e, __match_any_sync(0xffffffffu, e));
+    }
     for (int i = max(c0, all) + threadIdx.x; i < c1; i += kRankThreads) slot[i] = -1;  // behind the last expert
     cluster_wait();
 }
