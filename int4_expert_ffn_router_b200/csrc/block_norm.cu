@@ -517,6 +517,8 @@ __global__ void __launch_bounds__(1024) block_norm_wide_kernel(NormArgs a) {
 // m2 and du need ds only in sums, and ds is linear in three of them, so one
 // round of six sums a row is enough:
 //   s^2, s q dn, y^2, b y dxo, b y q dn, b y s:   sum b yh ds = rho (S3 + r (S4 - r m1 S5)).
+// Without `next` no output depends on s: it is not read (0 in its place), so that
+// infinities and NaN in it do not show.
 // A block keeps dq and A of its threads' columns over its rows in registers;
 // sum_parts_kernel adds the blocks'.
 // At 2048 x 6144 bf16 (151 MB): 36 us, of which the rows take 24 (6.3 TB/s), the
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
     const uint32_t ring = smem_addr(ring_mem);
     if constexpr (kRing)
         for (int i = 0; i < stages; ++i) {
-            ring_clear<XT, V, N>(ring + i * slot_bytes, false, H);
+            ring_clear<XT, V, N>(ring + i * slot_bytes, !has_next, H);
             ring_clear<YT, V, N>(ring + i * slot_bytes + yo, !has_prev, H);
             ring_clear<XT, V, N>(ring + i * slot_bytes + oo, !has_o, H);
             ring_clear<NT, V, N>(ring + i * slot_bytes + no, !has_next, H);
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
         if constexpr (kRing) {
             if (pt < a.T) {
                 const uint32_t at = ring + slot * slot_bytes;
-                ring_copy<XT, V, N>(at, (const XT*)a.x + (size_t)pt * a.ldx + c0, H);
+                if (has_next) ring_copy<XT, V, N>(at, (const XT*)a.x + (size_t)pt * a.ldx + c0, H);
                 if (has_prev) ring_copy<YT, V, N>(at + yo, (const YT*)a.y + (size_t)pt * a.ldy + c0, H);
                 if (has_o) ring_copy<XT, V, N>(at + oo, (const XT*)a.dxo + (size_t)pt * a.lddxo + c0, H);
                 if (has_next) ring_copy<NT, V, N>(at + no, (const NT*)a.dn + (size_t)pt * a.lddn + c0, H);
@@ -586,7 +588,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
     auto fetch = [&](int t) {
 #pragma unroll
         for (int i = 0; i < kKept; ++i) {
-            take<XT, V, false>(rs[i], true, i, 0, (const XT*)a.x + (size_t)t * a.ldx + c0, H);
+            take<XT, V, false>(rs[i], has_next, i, 0, (const XT*)a.x + (size_t)t * a.ldx + c0, H);
             take<YT, V, false>(ry[i], has_prev, i, 0, (const YT*)a.y + (size_t)t * a.ldy + c0, H);
             take<XT, V, false>(ro[i], has_o, i, 0, (const XT*)a.dxo + (size_t)t * a.lddxo + c0, H);
             take<NT, V, false>(rn[i], has_next, i, 0, (const NT*)a.dn + (size_t)t * a.lddn + c0, H);
@@ -623,7 +625,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
             } else {
                 const int k = kRing ? 0 : i;
                 if (kRing || pass == 0) {
-                    take<XT, V, kRing>(rs[k], true, i, at, (const XT*)a.x + (size_t)t * a.ldx + c0, H);
+                    take<XT, V, kRing>(rs[k], has_next, i, at, (const XT*)a.x + (size_t)t * a.ldx + c0, H);
                     take<YT, V, kRing>(ry[k], has_prev, i, at + yo, (const YT*)a.y + (size_t)t * a.ldy + c0, H);
                     take<XT, V, kRing>(ro[k], has_o, i, at + oo, (const XT*)a.dxo + (size_t)t * a.lddxo + c0, H);
                     take<NT, V, kRing>(rn[k], has_next, i, at + no, (const NT*)a.dn + (size_t)t * a.lddn + c0, H);
@@ -777,9 +779,11 @@ __global__ void __launch_bounds__(1024) block_norm_backward_wide_kernel(NormArgs
             s = y = n = o = 0.0f;
             float v[1];
             Raw<XT, 1> rx;
-            rx.load((const XT*)a.x + (size_t)t * a.ldx + c);
-            rx.get(v);
-            s = v[0];
+            if (a.has_next) {
+                rx.load((const XT*)a.x + (size_t)t * a.ldx + c);
+                rx.get(v);
+                s = v[0];
+            }
             if (a.dxo) {
                 rx.load((const XT*)a.dxo + (size_t)t * a.lddxo + c);
                 rx.get(v);
@@ -807,7 +811,7 @@ __global__ void __launch_bounds__(1024) block_norm_backward_wide_kernel(NormArgs
             w[2] += (double)y * y;
         }
         block_sum<double, 3>(w, red64[0]);
-        const float r = rms_scale(w[0], H, a.eps_pre);
+        const float r = a.has_next ? rms_scale(w[0], H, a.eps_pre) : 0.0f;
         const float m1 = (float)(w[1] * (double)r / H);
         const float rho = a.post_norm ? rms_scale(w[2], H, a.eps_post) : 1.0f;
         double v[1] = {0.0};
