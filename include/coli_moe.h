@@ -576,6 +576,7 @@ coli_status coli_block_norm(const coli_block_params* prev, const coli_block_para
  *   ds   = dx_out + d norm(s)^T (next.pre_gain * dn)
  *   dx   = prev.x_scale * ds  (prev NULL: ds)
  *   dy   = d post(y)^T (prev.y_scale * token_gate * prev.gate * ds)
+ *          (without post_norm no part of y: what it holds does not show in dy)
  * and, summed over the tokens, dpre_gain, dpost_gain, dgate [hidden], and
  * dtoken_gate [n_tokens] (each fp32, or NULL; dpost_gain needs post_norm).
  * x_out, dx_out, dx: x_dtype; y, dy: y_dtype; dn: n_dtype. dx and dy may be

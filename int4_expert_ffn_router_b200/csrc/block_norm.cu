@@ -720,7 +720,9 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
                 o[j] = __ffma2_rn(r2, __ffma2_rn(sh, m1n, __fmul2_rn(q[k], n[j])), o[j]);  // ds
                 const float2 uo = __fmul2_rn(u2, o[j]);
                 A[k] = __ffma2_rn(yh, uo, A[k]);
-                y[j] = __fmul2_rn(rho2, __ffma2_rn(yh, m2, __fmul2_rn(b[k], uo)));
+                float2 z = __fmul2_rn(b[k], uo);
+                if (post) z = __fmul2_rn(rho2, __ffma2_rn(yh, m2, z));  // else dy has no part of y, not even 0 y
+                y[j] = z;
                 o[j] = __fmul2_rn(both(a.xs), o[j]);
             }
             const int left = H - (int)(i * blockDim.x + threadIdx.x) * V;
@@ -838,7 +840,7 @@ __global__ void __launch_bounds__(1024) block_norm_backward_wide_kernel(NormArgs
                         out.store((XT*)a.dx + (size_t)t * a.lddx + c);
                     }
                     if (a.dy) {
-                        f[0] = rho * fmaf(-yh, m2, u * b * o);
+                        f[0] = a.post_norm ? rho * fmaf(-yh, m2, u * b * o) : u * b * o;
                         Raw<YT, 1> out;
                         out.set(f);
                         out.store((YT*)a.dy + (size_t)t * a.lddy + c);

@@ -52,3 +52,25 @@ def test_last_block_does_not_depend_on_x_out(gpu, coli, H, T, post, t):
         check_backward(got, ref.Norm(a, None, u).backward(ref.d(s), ref.d(y), ref.d(dxo), None), T, t, t)
     nothing = run_backward(coli, a, None, poisoned(s), y, None, None, u, t, t)  # no gradient comes in: none goes out
     assert all((v == 0).all() for v in nothing.values())
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("with_next", [True, False])
+@pytest.mark.parametrize("T", [3, 400])
+@pytest.mark.parametrize("H", WIDTHS)
+def test_dy_without_post_norm_does_not_depend_on_y(gpu, coli, H, T, with_next, t):
+    gen = torch.Generator().manual_seed(22)
+    s, y, dxo, dn = (view((T, H), DT[t], gpu, "dense", gen) for _ in range(4))
+    a, b = params(H, gpu, gen, post=False), params(H, gpu, gen) if with_next else None
+    u = torch.rand(T, generator=gen).to(gpu)
+    n = dn if with_next else None
+    got = run_backward(coli, a, b, s, poisoned(y), dxo, n, u, t, t)
+    r = ref.Norm(a, b, u)
+    want = r.backward(ref.d(s), torch.zeros((T, H), dtype=ref.D), ref.d(dxo), None if n is None else ref.d(n))
+    same = {k: got[k] for k in ("dx", "dy", "dpre") if k in got}
+    check_backward(same, want, T, t, t)
+    bad = torch.zeros(T, dtype=torch.bool, device=gpu)
+    bad[::2] = True
+    bad[T - 1] = True
+    # the sums over the columns of y do hold what y holds
+    assert not torch.isfinite(got["dtoken"][bad]).any() and torch.isfinite(got["dtoken"][~bad]).all()
