@@ -571,8 +571,8 @@ coli_status coli_block_norm(const coli_block_params* prev, const coli_block_para
 /*
  * Its gradient, from dx_out (d loss / d x_out by the paths other than n; NULL:
  * 0) and dn (d loss / d n). x_out is the forward's (with prev NULL: x) and y
- * its input; x is not needed. With next NULL no output depends on x_out, and
- * what it holds is not read. With s = x_out, ds the whole gradient on it:
+ * its input; x is not needed. With next NULL no output depends on x_out,
+ * whatever it holds. With s = x_out, ds the whole gradient on it:
  *   ds   = dx_out + d norm(s)^T (next.pre_gain * dn)
  *   dx   = prev.x_scale * ds  (prev NULL: ds)
  *   dy   = d post(y)^T (prev.y_scale * token_gate * prev.gate * ds)

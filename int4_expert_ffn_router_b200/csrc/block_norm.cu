@@ -517,8 +517,8 @@ __global__ void __launch_bounds__(1024) block_norm_wide_kernel(NormArgs a) {
 // m2 and du need ds only in sums, and ds is linear in three of them, so one
 // round of six sums a row is enough:
 //   s^2, s q dn, y^2, b y dxo, b y q dn, b y s:   sum b yh ds = rho (S3 + r (S4 - r m1 S5)).
-// Without `next` no output depends on s: it is not read (0 in its place), so that
-// infinities and NaN in it do not show.
+// Without `next` no output depends on s: it is 0 then, so that infinities and NaN in
+// x_out do not show.
 // A block keeps dq and A of its threads' columns over its rows in registers;
 // sum_parts_kernel adds the blocks'.
 // At 2048 x 6144 bf16 (151 MB): 36 us, of which the rows take 24 (6.3 TB/s), the
@@ -526,14 +526,17 @@ __global__ void __launch_bounds__(1024) block_norm_wide_kernel(NormArgs a) {
 // the rows took 50: what every warp repeats for a row (sums, factors, addresses)
 // is more than half of its instructions then.
 // ---------------------------------------------------------------------------
-template <typename XT, typename YT, typename NT, int V, int N>
+// post: without the post norm dy has no part of y, not even 0 y, so that infinities
+// and NaN in y do not show. (As a condition on every value it took 0.3 to 0.5 us of
+// the 36, and 3 % where rows are read by columns.)
+template <typename XT, typename YT, typename NT, int V, int N, bool post>
 __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs a) {
     __shared__ float red[2][16 * 8];
     __shared__ double red64[32 * 6];
     extern __shared__ __align__(16) unsigned char ring_mem[];
     constexpr bool kRing = V >= 4;
     const int H = a.H, stages = a.stages, c0 = threadIdx.x * V;
-    const bool has_prev = a.has_prev, has_next = a.has_next, has_o = a.dxo != nullptr, post = a.post_norm;
+    const bool has_prev = a.has_prev, has_next = a.has_next, has_o = a.dxo != nullptr;
     uint32_t yo = 0, oo = 0, no = 0, slot_bytes = 0;  // offsets of y, dxo and dn in a slot
     if constexpr (kRing) {
         yo = ring_bytes<XT, V, N>();
@@ -720,9 +723,8 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormArgs
                 o[j] = __ffma2_rn(r2, __ffma2_rn(sh, m1n, __fmul2_rn(q[k], n[j])), o[j]);  // ds
                 const float2 uo = __fmul2_rn(u2, o[j]);
                 A[k] = __ffma2_rn(yh, uo, A[k]);
-                float2 z = __fmul2_rn(b[k], uo);
-                if (post) z = __fmul2_rn(rho2, __ffma2_rn(yh, m2, z));  // else dy has no part of y, not even 0 y
-                y[j] = z;
+                y[j] = __fmul2_rn(b[k], uo);
+                if constexpr (post) y[j] = __fmul2_rn(rho2, __ffma2_rn(yh, m2, y[j]));
                 o[j] = __fmul2_rn(both(a.xs), o[j]);
             }
             const int left = H - (int)(i * blockDim.x + threadIdx.x) * V;
@@ -781,11 +783,9 @@ __global__ void __launch_bounds__(1024) block_norm_backward_wide_kernel(NormArgs
             s = y = n = o = 0.0f;
             float v[1];
             Raw<XT, 1> rx;
-            if (a.has_next) {
-                rx.load((const XT*)a.x + (size_t)t * a.ldx + c);
-                rx.get(v);
-                s = v[0];
-            }
+            rx.load((const XT*)a.x + (size_t)t * a.ldx + c);
+            rx.get(v);
+            s = v[0];
             if (a.dxo) {
                 rx.load((const XT*)a.dxo + (size_t)t * a.lddxo + c);
                 rx.get(v);
@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(1024) block_norm_backward_wide_kernel(NormArgs
             w[2] += (double)y * y;
         }
         block_sum<double, 3>(w, red64[0]);
-        const float r = a.has_next ? rms_scale(w[0], H, a.eps_pre) : 0.0f;
+        const float r = rms_scale(w[0], H, a.eps_pre);  // without next it and s, sh and m1 show in no output
         const float m1 = (float)(w[1] * (double)r / H);
         const float rho = a.post_norm ? rms_scale(w[2], H, a.eps_post) : 1.0f;
         double v[1] = {0.0};
@@ -840,7 +840,8 @@ __global__ void __launch_bounds__(1024) block_norm_backward_wide_kernel(NormArgs
                         out.store((XT*)a.dx + (size_t)t * a.lddx + c);
                     }
                     if (a.dy) {
-                        f[0] = a.post_norm ? rho * fmaf(-yh, m2, u * b * o) : u * b * o;
+                        f[0] = u * b * o;
+                        if (a.post_norm) f[0] = rho * fmaf(-yh, m2, f[0]);
                         Raw<YT, 1> out;
                         out.set(f);
                         out.store((YT*)a.dy + (size_t)t * a.lddy + c);
@@ -963,22 +964,22 @@ cudaError_t forward_typed(NormArgs& a, int V, cudaStream_t st) {
     return launch_rows(k, a, s, sizeof(XT) + sizeof(YT), s.N ? grid_of(a.T, a.H, true) : a.T, true, st);
 }
 
-template <typename XT, typename YT, typename NT>
+template <typename XT, typename YT, typename NT, bool post>
 cudaError_t backward_typed(NormArgs& a, int V, cudaStream_t st) {
     constexpr bool narrow = sizeof(XT) + sizeof(YT) + sizeof(NT) == 6;
     const Shape s = shape_of(a.H, V);
     Kernel k = block_norm_backward_wide_kernel<XT, YT, NT>;
     if (s.N && V == 8) {
-        if constexpr (narrow) k = s.N == 1 ? block_norm_backward_kernel<XT, YT, NT, 8, 1> : block_norm_backward_kernel<XT, YT, NT, 8, 2>;
+        if constexpr (narrow) k = s.N == 1 ? block_norm_backward_kernel<XT, YT, NT, 8, 1, post> : block_norm_backward_kernel<XT, YT, NT, 8, 2, post>;
     } else if (s.N && V == 4) {
-        k = s.N == 1   ? block_norm_backward_kernel<XT, YT, NT, 4, 1>
-            : s.N == 2 ? block_norm_backward_kernel<XT, YT, NT, 4, 2>
-                       : block_norm_backward_kernel<XT, YT, NT, 4, 4>;
+        k = s.N == 1   ? block_norm_backward_kernel<XT, YT, NT, 4, 1, post>
+            : s.N == 2 ? block_norm_backward_kernel<XT, YT, NT, 4, 2, post>
+                       : block_norm_backward_kernel<XT, YT, NT, 4, 4, post>;
     } else if (s.N) {
-        k = s.N == 1   ? block_norm_backward_kernel<XT, YT, NT, 2, 1>
-            : s.N == 2 ? block_norm_backward_kernel<XT, YT, NT, 2, 2>
-            : s.N == 4 ? block_norm_backward_kernel<XT, YT, NT, 2, 4>
-                       : block_norm_backward_kernel<XT, YT, NT, 2, 8>;
+        k = s.N == 1   ? block_norm_backward_kernel<XT, YT, NT, 2, 1, post>
+            : s.N == 2 ? block_norm_backward_kernel<XT, YT, NT, 2, 2, post>
+            : s.N == 4 ? block_norm_backward_kernel<XT, YT, NT, 2, 4, post>
+                       : block_norm_backward_kernel<XT, YT, NT, 2, 8, post>;
     }
     return launch_rows(k, a, s, 2 * sizeof(XT) + sizeof(YT) + sizeof(NT), grid_of(a.T, a.H, false), false, st);
 }
@@ -987,7 +988,8 @@ template <bool fwd>
 cudaError_t by_type(NormArgs& a, coli_dtype xt, coli_dtype yt, coli_dtype nt, int V, cudaStream_t st) {
     auto go = [&](auto x, auto y, auto n) {
         if constexpr (fwd) return forward_typed<decltype(x), decltype(y), decltype(n)>(a, V, st);
-        else return backward_typed<decltype(x), decltype(y), decltype(n)>(a, V, st);
+        else return a.post_norm ? backward_typed<decltype(x), decltype(y), decltype(n), true>(a, V, st)
+                                : backward_typed<decltype(x), decltype(y), decltype(n), false>(a, V, st);
     };
     auto with_n = [&](auto x, auto y) { return nt == COLI_F32 ? go(x, y, float()) : go(x, y, B()); };
     auto with_y = [&](auto x) { return yt == COLI_F32 ? with_n(x, float()) : with_n(x, B()); };
