@@ -32,7 +32,6 @@ struct NormArgs {
 // A sum of squares that fp32 holds well: it neither overflowed nor lost to
 // underflow anything that eps does not hide (a square below 2^-126 is lost).
 __device__ __forceinline__ bool sum_ok(float ss, float eps) { return ss <= 3e37f && (ss >= 1e-24f || eps >= 1e-12f); }
-__device__ __forceinline__ float rms_scale(float ss, int H, float eps) { return rsqrtf(ss / (float)H + eps); }
 __device__ __forceinline__ float rms_scale(double ss, int H, float eps) { return (float)(1.0 / sqrt(ss / H + (double)eps)); }
 
 // A column's gain or gate (NULL: 1).
@@ -421,16 +420,17 @@ __global__ void __launch_bounds__(kForwardThreads) block_norm_kernel(const NormA
 }
 
 // Rows too wide for registers: the same sums over columns that a thread reads
-// again from memory (x_out again after it stored it, by the same thread).
+// again from memory (x_out again after it stored it, by the same thread). In fp64:
+// a thread adds up to 128 columns one after another, which in fp32 could lose 60
+// steps of 2^-24 of 1 / rms where the narrow rows' sums lose 18 at most.
 template <typename XT, typename YT, typename NT>
 __global__ void __launch_bounds__(1024) block_norm_wide_kernel(NormArgs a) {
-    __shared__ float red[2][32];
     __shared__ double red64[2][32];
     const int t = blockIdx.x, H = a.H;
     const XT* x = (const XT*)a.x + (size_t)t * a.ldx;
     const YT* y = (const YT*)a.y + (size_t)t * a.ldy;
     XT* xo = a.has_prev ? (XT*)a.xo + (size_t)t * a.ldxo : nullptr;
-    float ss[1] = {0.0f};
+    double ss[1] = {0.0};
     if (a.has_prev) {
         float rho = 1.0f;
         if (a.post_norm) {
@@ -439,25 +439,13 @@ __global__ void __launch_bounds__(1024) block_norm_wide_kernel(NormArgs a) {
                 r.load(y + c);
                 float v[1];
                 r.get(v);
-                ss[0] = fmaf(v[0], v[0], ss[0]);
+                ss[0] += (double)v[0] * v[0];
             }
-            block_sum<float, 1>(ss, red[0]);
+            block_sum<double, 1>(ss, red64[0]);
             rho = rms_scale(ss[0], H, a.eps_post);
-            if (!sum_ok(ss[0], a.eps_post)) {
-                double dd[1] = {0.0};
-                for (int c = threadIdx.x; c < H; c += blockDim.x) {
-                    Raw<YT, 1> r;
-                    r.load(y + c);
-                    float v[1];
-                    r.get(v);
-                    dd[0] += (double)v[0] * v[0];
-                }
-                block_sum<double, 1>(dd, red64[0]);
-                rho = rms_scale(dd[0], H, a.eps_post);
-            }
         }
         const float scale = a.ys * (a.token ? a.token[t] : 1.0f);
-        ss[0] = 0.0f;
+        ss[0] = 0.0;
         for (int c = threadIdx.x; c < H; c += blockDim.x) {
             Raw<XT, 1> rx;
             Raw<YT, 1> ry;
@@ -470,7 +458,7 @@ __global__ void __launch_bounds__(1024) block_norm_wide_kernel(NormArgs a) {
             rx.set(vx);
             rx.store(xo + c);
             rx.get(vx);
-            ss[0] = fmaf(vx[0], vx[0], ss[0]);
+            ss[0] += (double)vx[0] * vx[0];
         }
         x = xo;
     } else {
@@ -479,24 +467,12 @@ __global__ void __launch_bounds__(1024) block_norm_wide_kernel(NormArgs a) {
             rx.load(x + c);
             float v[1];
             rx.get(v);
-            ss[0] = fmaf(v[0], v[0], ss[0]);
+            ss[0] += (double)v[0] * v[0];
         }
     }
     if (!a.has_next) return;
-    block_sum<float, 1>(ss, red[1]);
-    float r = rms_scale(ss[0], H, a.eps_pre);
-    if (!sum_ok(ss[0], a.eps_pre)) {
-        double dd[1] = {0.0};
-        for (int c = threadIdx.x; c < H; c += blockDim.x) {
-            Raw<XT, 1> rx;
-            rx.load(x + c);
-            float v[1];
-            rx.get(v);
-            dd[0] += (double)v[0] * v[0];
-        }
-        block_sum<double, 1>(dd, red64[1]);
-        r = rms_scale(dd[0], H, a.eps_pre);
-    }
+    block_sum<double, 1>(ss, red64[1]);
+    const float r = rms_scale(ss[0], H, a.eps_pre);
     for (int c = threadIdx.x; c < H; c += blockDim.x) {
         Raw<XT, 1> rx;
         rx.load(x + c);
