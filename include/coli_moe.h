@@ -597,8 +597,12 @@ coli_status coli_block_norm_backward(const coli_block_params* prev, const coli_b
  * activations, in place: for l = 0..n_layers-1
  *   x <- x_scale_l * x + y_scale_l * gate_l * post_l(MoE_l(norm(x) * pre_gain_l))
  * blocks: host array of n_layers parameters. y_work [n_tokens][H] fp32 DEVICE
- * scratch, not overlapping x. Otherwise as coli_moe_stack_forward; the end of
- * a block and the start of the next are one pass (coli_block_norm).
+ * scratch, not overlapping x. Every layer must hold all its experts: a layer of
+ * coli_moe_layer_create_ep with world > 1 is refused (COLI_EINVAL), since the
+ * norms and the next router need the sum over the ranks; call such layers one by
+ * one, with coli_block_norm and the all-reduce between them. Otherwise as
+ * coli_moe_stack_forward; the end of a block and the start of the next are one
+ * pass (coli_block_norm).
  */
 coli_status coli_moe_block_stack_forward(coli_moe_layer* const* layers, const coli_block_params* blocks, int n_layers,
                                          float* x, float* y_work, int n_tokens, coli_stream stream);

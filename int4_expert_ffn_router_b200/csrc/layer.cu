@@ -890,6 +890,9 @@ COLI_API coli_status coli_moe_stack_forward(coli_moe_layer* const* layers, int n
     return COLI_OK;
 }
 
+// Whether a layer's output is the whole output (expert parallelism: one rank's part).
+static bool holds_all(const coli_moe_layer* L) { return L->ep_lo == 0 && L->ep_hi == L->d.E; }
+
 COLI_API coli_status coli_moe_block_stack_forward(coli_moe_layer* const* layers, const coli_block_params* blocks,
                                                   int n_layers, float* x, float* y_work, int T, coli_stream stream) {
     if (!layers || !blocks || n_layers < 0) return fail(COLI_EINVAL, "bad layer or block list");
@@ -902,6 +905,8 @@ COLI_API coli_status coli_moe_block_stack_forward(coli_moe_layer* const* layers,
         if (st != COLI_OK) return st;
         if (layers[l]->d.H != L0->d.H || layers[l]->device != L0->device)
             return fail(COLI_EINVAL, "layers must share hidden size and device");
+        // another rank's experts would be missing from what the norms and the next routers see
+        if (!holds_all(layers[l])) return fail(COLI_EINVAL, "a layer of the stack holds a part of the experts only");
         if (const char* m = check_block_params(blocks + l)) return fail(COLI_EINVAL, m);
     }
     const int H = L0->d.H;
