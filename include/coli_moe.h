@@ -255,7 +255,9 @@ coli_status coli_moe_forward(coli_moe_layer* layer, const void* x, void* y, coli
  * Residual stack over fp32 activations, in place:
  *   x <- x + MoE_l(RMSNorm(x)) for l = 0..n_layers-1,
  * RMSNorm with unit gain: x / sqrt(mean(x^2) + eps). All layers must share
- * H and live on one device; n_tokens <= every layer's max_tokens.
+ * H and live on one device; n_tokens <= every layer's max_tokens. A layer of
+ * coli_moe_layer_create_ep with world > 1 adds its rank's part only, so it may
+ * only be the last one (COLI_EINVAL before another layer).
  */
 coli_status coli_moe_stack_forward(coli_moe_layer* const* layers, int n_layers, float* x, int n_tokens,
                                    float eps, coli_stream stream);

@@ -865,6 +865,9 @@ COLI_API coli_status coli_moe_forward(coli_moe_layer* L, const void* x, void* y,
     return forward_impl(L, x, y, dt, T, nullptr, (cudaStream_t)stream);
 }
 
+// Whether a layer's output is the whole output (expert parallelism: one rank's part).
+static bool holds_all(const coli_moe_layer* L) { return L->ep_lo == 0 && L->ep_hi == L->d.E; }
+
 COLI_API coli_status coli_moe_stack_forward(coli_moe_layer* const* layers, int n_layers, float* x, int T, float eps,
                                             coli_stream stream) {
     if (!layers || n_layers < 0) return fail(COLI_EINVAL, "bad layer list");
@@ -876,6 +879,9 @@ COLI_API coli_status coli_moe_stack_forward(coli_moe_layer* const* layers, int n
         if (st != COLI_OK) return st;
         if (layers[l]->d.H != L0->d.H || layers[l]->device != L0->device)
             return fail(COLI_EINVAL, "layers must share hidden size and device");
+        // the layers behind it would see an x that lacks the other ranks' experts
+        if (l + 1 < n_layers && !holds_all(layers[l]))
+            return fail(COLI_EINVAL, "a layer before the last holds a part of the experts only");
     }
     DeviceGuard guard(L0->device);
     cudaStream_t s = (cudaStream_t)stream;
@@ -889,9 +895,6 @@ COLI_API coli_status coli_moe_stack_forward(coli_moe_layer* const* layers, int n
     }
     return COLI_OK;
 }
-
-// Whether a layer's output is the whole output (expert parallelism: one rank's part).
-static bool holds_all(const coli_moe_layer* L) { return L->ep_lo == 0 && L->ep_hi == L->d.E; }
 
 COLI_API coli_status coli_moe_block_stack_forward(coli_moe_layer* const* layers, const coli_block_params* blocks,
                                                   int n_layers, float* x, float* y_work, int T, coli_stream stream) {

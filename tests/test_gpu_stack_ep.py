@@ -50,3 +50,34 @@ def test_block_stack_of_one_rank_that_holds_all(gpu, coli):
     assert torch.equal(a, b) and not torch.equal(a, x)
     full.close()
     one.close()
+
+
+@pytest.mark.parametrize("rank", [0, 1])
+def test_stack_refuses_a_part_of_the_experts_before_another_layer(gpu, coli, rank):
+    layers = [layer(coli, 0, (rank, 2)), layer(coli, 1)]
+    x = torch.from_numpy(synth.x_f32(5, 0, T, H)).to(gpu)
+    before = x.clone()
+    with pytest.raises(coli.ColiError, match="experts"):
+        coli.stack_forward(layers, x)
+    torch.cuda.synchronize()
+    assert torch.equal(x, before)
+    for l in layers:
+        l.close()
+
+
+def test_stack_that_ends_in_a_part_of_the_experts(gpu, coli):
+    """The last layer adds its part to x: over the ranks, the parts sum to the whole layer's output (1e-5 of the
+    largest value, as in test_gpu_ep: the order of the fp32 additions)."""
+    first, full = layer(coli, 0), layer(coli, 1)
+    ranks = [layer(coli, 1, (r, 2)) for r in range(2)]
+    x = torch.from_numpy(synth.x_f32(5, 0, T, H)).to(gpu)
+    runs = []
+    for last in (full, *ranks):
+        runs.append(x.clone())
+        coli.stack_forward([first, last], runs[-1])
+    mid = x.clone()
+    coli.stack_forward([first], mid)
+    whole, a, b, mid = (r.double() for r in (*runs, mid))
+    assert float((a + b - mid - whole).abs().max()) <= 1e-5 * float(whole.abs().max())
+    for l in (first, full, *ranks):
+        l.close()
