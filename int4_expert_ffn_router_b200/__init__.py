@@ -367,7 +367,10 @@ def stack_forward(layers, x, n_tokens: int | None = None, eps: float = 1e-6, str
 # matrices are [rows][hidden], float32 or bfloat16, with any distance between
 # rows; index and gain arrays are contiguous int32 / float32. Outputs are the
 # caller's; without `stream` the call goes to the current stream of the
-# tensors' device.
+# tensors' device. The calls record no gradient (their gradients are operators
+# of their own); they move the versions of the tensors that they write, so
+# autograd notices when a tensor that it saved is overwritten. On another
+# stream than the tensors' own the caller keeps them alive (record_stream).
 # ---------------------------------------------------------------------------
 _OPS = None
 
@@ -525,6 +528,8 @@ def block_stack_forward(layers, blocks, x, y_work, n_tokens: int | None = None, 
     _check(lib.coli_moe_block_stack_forward(ctypes.cast(arr, ctypes.c_void_p), ctypes.cast(par, ctypes.c_void_p),
                                             len(layers), _ptr(x), _ptr(y_work), T, _stream(stream, dev)),
            "coli_moe_block_stack_forward")
+    import torch
+    torch.autograd.graph.increment_version([x, y_work])
 
 
 def debug_fail_alloc(nth: int) -> None:

@@ -11,6 +11,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
 #include <string>
 
 #include "../../include/coli_moe.h"
@@ -180,13 +181,26 @@ int64_t width_of(const at::Tensor& t, const char* name) {
     return sized(t.size(1), name);
 }
 
+// A tensor argument was written: its version moves, as with torch's in-place
+// operations, so that autograd notices if it had saved the values. (A tensor of
+// inference mode has no version.)
+void written(PyObject* o) {
+    if (o == Py_None) return;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // Runs f (which makes one library call through `call`) and returns its status
-// to Python. Nothing within `call` may throw: the interpreter's lock is released there.
+// to Python; `outs`: the arguments that it writes. Nothing within `call` may
+// throw: the interpreter's lock is released there.
 template <typename F>
-PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F f) {
+PyObject* guarded(PyObject* const* a, Py_ssize_t given, Py_ssize_t wanted, std::initializer_list<int> outs, F f) {
     try {
         if (given != wanted) type_error("wrong number of arguments");
-        return PyLong_FromLong((long)f());
+        const coli_status st = f();
+        if (st == COLI_OK)
+            for (int i : outs) written(a[i]);
+        return PyLong_FromLong((long)st);
     } catch (const Refused& r) {
         PyErr_SetString(r.type, r.msg.c_str());
     } catch (const std::exception& e) {
@@ -206,7 +220,7 @@ coli_status call(F f) {
 
 // ids, x, n_experts, counts, offsets, pos, slot, rows, work, stream
 ENTRY(dispatch) {
-    return guarded(n, 10, [&] {
+    return guarded(a, n, 10, {3, 4, 5, 6, 7, 8}, [&] {
         const Slots s = slots_of(a[0], "ids");
         const int E = sized(integer(a[2], "n_experts"), "n_experts");
         const at::Tensor* x = tensor(a[1], "x");
@@ -232,7 +246,7 @@ Mat base_of(PyObject* o, const Mat& out, int64_t T, int64_t H, int dev) {
 
 // pos, drows, dx, base, stream
 ENTRY(dispatch_backward) {
-    return guarded(n, 5, [&] {
+    return guarded(a, n, 5, {2}, [&] {
         const Slots s = slots_of(a[0], "pos");
         const int64_t H = width_of(required(a[2], "dx"), "dx");
         required(a[1], "drows");
@@ -249,7 +263,7 @@ ENTRY(dispatch_backward) {
 
 // pos, weights, rows, y, base, stream
 ENTRY(combine) {
-    return guarded(n, 6, [&] {
+    return guarded(a, n, 6, {3}, [&] {
         const Slots s = slots_of(a[0], "pos");
         const int64_t H = width_of(required(a[3], "y"), "y");
         required(a[2], "rows");
@@ -267,7 +281,7 @@ ENTRY(combine) {
 
 // pos, weights, dy, rows, drows, dweights, stream
 ENTRY(combine_backward) {
-    return guarded(n, 7, [&] {
+    return guarded(a, n, 7, {4, 5}, [&] {
         const Slots s = slots_of(a[0], "pos");
         const int64_t H = width_of(required(a[2], "dy"), "dy");
         const int32_t* pos = ints(a[0], "pos", s.dev, s.T, s.K);
@@ -288,7 +302,7 @@ ENTRY(combine_backward) {
 
 // router_w, x, ids, weights, dweights, offsets, slot, dlogits, dx, drouter_w, dbias, work, stream
 ENTRY(route_backward) {
-    return guarded(n, 13, [&] {
+    return guarded(a, n, 13, {7, 8, 9, 10, 11}, [&] {
         const Slots s = slots_of(a[2], "ids");
         const at::Tensor& wr = required(a[0], "router_w");
         const int64_t H = width_of(wr, "router_w"), E = sized(wr.size(0), "router_w");
@@ -311,7 +325,7 @@ ENTRY(route_backward) {
 
 // prev, next, x, y, x_out, n, token_gate, stream
 ENTRY(block_norm) {
-    return guarded(n, 8, [&] {
+    return guarded(a, n, 8, {4, 5}, [&] {
         const at::Tensor& tx = required(a[2], "x");
         const int dev = (int)tx.get_device();
         const int64_t H = width_of(tx, "x");
@@ -331,7 +345,7 @@ ENTRY(block_norm) {
 
 // prev, next, x_out, y, dx_out, dn, dx, dy, dpre_gain, dpost_gain, dgate, token_gate, dtoken_gate, work, stream
 ENTRY(block_norm_backward) {
-    return guarded(n, 15, [&] {
+    return guarded(a, n, 15, {6, 7, 8, 9, 10, 12, 13}, [&] {
         const at::Tensor& ts = required(a[2], "x_out");
         const int dev = (int)ts.get_device();
         const int64_t H = width_of(ts, "x_out");
