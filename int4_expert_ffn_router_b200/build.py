@@ -12,6 +12,7 @@ BINDING_SO = os.path.join(HERE, "_binding.so")
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
     "-Xcompiler", "-fPIC,-fvisibility=hidden", "-shared", "--expt-relaxed-constexpr",
+    "-Xlinker", "-soname=" + os.path.basename(SO),  # a name, not this machine's path, in what links to it
 ]
 
 
@@ -31,7 +32,8 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
 
 
 def build_binding(verbose: bool = False) -> str:
-    """The Python module of the operators on torch tensors (csrc/binding.cpp), linked to libcoli_moe.so beside it."""
+    """The Python module of the operators on torch tensors (csrc/binding.cpp), linked by name to the libcoli_moe.so
+    beside it: a copied or moved package runs its own library."""
     import importlib.util
     import sysconfig
 
@@ -42,7 +44,7 @@ def build_binding(verbose: bool = False) -> str:
     lib = os.path.join(torch, "lib")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            *(x for i in inc for x in ("-isystem", i)),
-           os.path.join(HERE, "csrc", "binding.cpp"), "-o", BINDING_SO, SO, "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch",
+           os.path.join(HERE, "csrc", "binding.cpp"), "-o", BINDING_SO, "-L" + HERE, "-l:" + os.path.basename(SO), "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch",
            "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd))
