@@ -31,13 +31,25 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     return SO
 
 
-def build_binding(verbose: bool = False) -> str:
+def build_binding(verbose: bool = False) -> str | None:
     """The Python module of the operators on torch tensors (csrc/binding.cpp), linked by name to the libcoli_moe.so
-    beside it: a copied or moved package runs its own library."""
+    beside it: a copied or moved package runs its own library. Only these operators need it: without torch, its CUDA
+    libraries or Python's headers it is left out (None), and the C library and its ctypes layer are all there is."""
     import importlib.util
     import sysconfig
 
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    missing = None
+    if spec is None or not spec.origin:
+        missing = "torch is not installed"
+    elif not glob.glob(os.path.join(os.path.dirname(spec.origin), "lib", "libc10_cuda.so*")):
+        missing = "torch was built without CUDA"
+    elif not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        missing = "Python.h is not installed"
+    if missing:
+        print(f"{os.path.basename(BINDING_SO)} is not built: {missing}; the operators on torch tensors are not available")
+        return None
+    torch = os.path.dirname(spec.origin)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
