@@ -462,8 +462,9 @@ coli_status coli_moe_route_noalloc(const float* router_w, const float* router_bi
  *    Results are deterministic: no atomics on values, fixed orders of summation.
  *  - `work` is scratch memory of the caller's, 16-byte aligned, at least as
  *    large as the operator's workspace function says (a NULL work where that
- *    is 0), of any contents. It carries nothing from one call to the next, but
- *    two calls that may overlap on the GPU must not share it.
+ *    is 0), of any contents. What it says for a number of tokens is enough for
+ *    fewer tokens too. It carries nothing from one call to the next, but two
+ *    calls that may overlap on the GPU must not share it.
  */
 
 /*

@@ -662,8 +662,10 @@ using namespace coli;
 
 COLI_API int64_t coli_moe_dispatch_workspace(int T, int K, int E) {
     if (check_slots(T, K) || E < 1 || E > kMaxExperts) return -1;
-    const int64_t n = (int64_t)T * K;
-    return n > kClusterSlots ? (int64_t)chunks_of(n).n * E * 4 : 0;
+    const int64_t n = (int64_t)T * K, chunks = (n + kChunkSlots - 1) / kChunkSlots;
+    // the most chunks that so many slots or fewer are cut into (just above kMaxChunks * kChunkSlots slots there are
+    // fewer, larger ones)
+    return n > kClusterSlots ? (chunks < kMaxChunks ? chunks : kMaxChunks) * E * 4 : 0;
 }
 
 COLI_API coli_status coli_moe_dispatch(const int32_t* ids, int T, int K, int E, const void* x, coli_dtype x_dtype,
@@ -689,7 +691,7 @@ COLI_API coli_status coli_moe_dispatch(const int32_t* ids, int T, int K, int E, 
         TRY_ARG(check_mat(mr, "rows is NULL", "rows_stride is smaller than hidden", "rows is not aligned to its element"));
         REQUIRE(!overlap(mx, mr), "x and rows overlap");
     }
-    const int64_t need = coli_moe_dispatch_workspace(T, K, E);
+    const int64_t need = n > kClusterSlots ? (int64_t)chunks_of((int64_t)n).n * E * 4 : 0;
     REQUIRE(need == 0 || (work && work_bytes >= need), "work is smaller than coli_moe_dispatch_workspace");
     REQUIRE(((uintptr_t)work & 15u) == 0, "work must be 16-byte aligned");
     const void* outs[] = {counts, offsets, pos, slot, move ? rows : nullptr, need ? work : nullptr};
