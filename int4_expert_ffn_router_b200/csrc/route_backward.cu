@@ -480,11 +480,14 @@ __global__ void __launch_bounds__(256) route_sum_kernel(const float* part, int s
 struct Cut {
     int chunk, n_chunks, per, splits;
 };
-Cut cut_of(int T, int K, int E, int H) {
+int most_splits(int T, int H) {
     const int slabs = (H + 127) / 128;
     int n = kSms / slabs;
     if (n > (T + 127) / 128) n = (T + 127) / 128;
-    if (n < 1) n = 1;
+    return n < 1 ? 1 : n;
+}
+Cut cut_of(int T, int K, int E, int H) {
+    const int n = most_splits(T, H);
     Cut c;
     const int share = T > 0 ? (T + n - 1) / n : 1, most = chunk_of(K, E);
     c.per = (share + most - 1) / most;
@@ -505,6 +508,14 @@ Layout layout_of(const Cut& c, int T, int K, int E, int H) {
     l.bound = l.inv + up((int64_t)T * K);
     l.total = l.bound + up((int64_t)(c.n_chunks + 1) * E);
     return l;
+}
+// Words that hold the layout of so many tokens or fewer. Both numbers grow with T
+// and are at least the cut's own (which may fall: 18945 tokens of 128 columns take
+// 147 splits, 18944 take 148): splits <= n, and n_chunks <= n per
+// <= n (ceil(T / n) / most + 1) <= (T + n) / most + n.
+int64_t most_words(int T, int K, int E, int H) {
+    const int n = most_splits(T, H);
+    return layout_of(Cut{0, (T + n) / chunk_of(K, E) + n, 0, n}, T, K, E, H).total;
 }
 
 // Columns of a slab of all E router rows (and the zero row) in shared memory, in warps' widths.
@@ -572,7 +583,7 @@ COLI_API int64_t coli_moe_route_backward_workspace(int T, int K, int E, int H) {
     if (T < 0 || T > kBlockMaxTokens || K < 1 || K > 32 || (int64_t)T * K > kBlockMaxSlots || E < 1 || E > 1024 || H < 1 ||
         H > kBlockMaxHidden)
         return -1;
-    return T > 0 ? layout_of(cut_of(T, K, E, H), T, K, E, H).total * 4 : 0;
+    return T > 0 ? most_words(T, K, E, H) * 4 : 0;
 }
 
 COLI_API coli_status coli_moe_route_backward(const float* router_w, int E, int H, int K, const void* x, coli_dtype dtype,
@@ -585,7 +596,7 @@ COLI_API coli_status coli_moe_route_backward(const float* router_w, int E, int H
     const int64_t size = coli_moe_route_backward_workspace(T, K, E, H);
     REQUIRE(size >= 0, "need 0 <= n_tokens <= 2^20, 1 <= top_k <= 32, n_tokens * top_k <= 2^24, 1 <= n_experts <= 1024, "
                        "1 <= hidden <= 65536");
-    const int64_t need = rows && T > 0 ? size : 0;
+    const int64_t need = rows && T > 0 ? layout_of(cut_of(T, K, E, H), T, K, E, H).total * 4 : 0;
     REQUIRE(dtype_ok(dtype), "dtype must be COLI_F32 or COLI_BF16");
     REQUIRE(device >= 0, "no such CUDA device");
     REQUIRE(need == 0 || (work && work_bytes >= need), "work is smaller than coli_moe_route_backward_workspace");
