@@ -445,15 +445,19 @@ coli_status coli_moe_route_noalloc(const float* router_w, const float* router_bi
 /*
  * Operators around the layer, for callers that run experts of their own (in
  * bf16, with adapters, in training) beside or instead of the int4 ones, and
- * for blocks whose norms carry gains, gates and scales. None of them needs a
- * layer or allocates; none synchronises; all can be captured in a CUDA graph.
+ * for blocks whose norms carry gains, gates and scales. But for the stack at the
+ * end none of them needs a layer; none allocates or synchronises, and all can be
+ * captured in a CUDA graph (the stack as its layers' forwards).
  * Common to them:
  *  - tensors are DEVICE pointers on `device`; a call switches to that device
  *    and back. `stream` is one of that device's streams.
  *  - matrices are row-major with `*_stride` elements between rows (>= the
  *    row's length); fp32 or bf16 (coli_dtype) as their dtype argument says,
- *    aligned to their element; rows that all start on 16-byte boundaries, with
- *    hidden % 8 == 0, take the vector path. int32 and fp32 arrays are dense.
+ *    aligned to their element. Any start and stride is right; the wider the
+ *    accesses that all matrices of a call allow (16, 8 or, but for the norms, 4
+ *    bytes: hidden a multiple of 8, 4 or 2, every row starting on such a
+ *    boundary), the faster. Norms of more than 8192 columns read them one at a
+ *    time. int32 and fp32 arrays are dense.
  *  - 0 <= n_tokens <= 2^20, 1 <= top_k <= 32, n_tokens * top_k <= 2^24,
  *    1 <= n_experts <= 1024, 1 <= hidden <= 65536.
  *  - an output must not overlap an input or another output unless a call says
@@ -564,7 +568,8 @@ typedef struct {
  * NULL: 1. prev NULL (before the first block): n = norm(x) * next.pre_gain; y,
  * x_out and token_gate must be NULL. next NULL (after the last block): n must
  * be NULL. x_out may be x, n may be y (same pointer, type and stride).
- * A mean of squares outside fp32's range is summed again in fp64.
+ * A mean of squares outside fp32's range is summed again in fp64; 1 / rms itself
+ * is fp32 (with eps 0, a row whose rms is below 3e-39 gives infinities).
  */
 coli_status coli_block_norm(const coli_block_params* prev, const coli_block_params* next, const void* x,
                             coli_dtype x_dtype, int64_t x_stride, const void* y, coli_dtype y_dtype, int64_t y_stride,

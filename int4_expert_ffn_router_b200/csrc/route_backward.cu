@@ -91,9 +91,9 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 // slab of 32 * VC columns of all E rows in shared memory and takes a share of
 // the tokens; a warp takes four tokens at a time (K <= 8), a lane VC columns of each.
 // The slots' rows and factors go through a buffer of the warp's, from which
-// all lanes read two slots with one access. Bound by shared memory reads (36
-// wavefronts a token and slab): 20 us there, where gathering the rows from L2
-// took 45. A slot that is absent reads a row of zeros.
+// all lanes read two slots with one access. Most of its time are shared memory
+// reads, 36 wavefronts a token and slab (13 of the 20 us there); gathering the
+// rows from L2 took 45. A slot that is absent reads a row of zeros.
 // ---------------------------------------------------------------------------
 struct SlotRef {
     int row;  // its row's place in shared memory, in elements or bytes
@@ -239,9 +239,11 @@ __device__ __forceinline__ void route_dx_block(const Dx& a, XT* dx, int bx, int 
 // adds its rows in order, a lane 8 bytes of each. A block takes `per` chunks of
 // its split one after another; its sums go to the split's part of the
 // workspace, which route_sum_kernel adds in order; with one split they are the
-// result. Bound by instructions, most of them widening and adding the 201 MB of
-// rows: 22 us at 2048 x 8 x 6144 bf16, 256 experts. (A block per expert that
-// walked its slots took 1200: the hottest expert has most tokens.)
+// result. 22 us at 2048 x 8 x 6144 bf16, 256 experts. (A block per expert that
+// walked its slots took 1200: the hottest expert has most tokens.) No unit is full:
+// with dx, 56 % of the issue slots and 58 % of the shared memory pipe are in use,
+// and warps wait for shared memory most; one block an SM has nothing to run while
+// it fills its chunk or waits at its barriers.
 // ---------------------------------------------------------------------------
 constexpr int kRowBytes = 256;
 constexpr int kRoom = 224 * 1024;        // shared memory of a chunk
